@@ -77,7 +77,8 @@ def draw(rng):
     mask = rng.random() < 0.5
     if op == "balance":
         return {"op": op, "T": min(T, 16384 * 128 // E), "E": E, "k": k, "mask": mask}
-    if op == "gate":
+    if op == "gate":      # one expert alone has weight 1 and no gradient
+        k = max(k, 2)
         return {"op": op, "T": min(T, 4096 * 20 * 2880 // (k * d)), "E": E, "k": k, "d": d, "mask": mask}
     if op == "router":
         return {"op": op, "T": min(T, 16384 * 128 // E), "E": E, "d": d, "rows": rng.choice(["bf16", "8bit"]),
