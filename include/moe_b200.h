@@ -482,6 +482,154 @@ MOE_API moe_status moe_rms_norm(const void* h_dev, const float* g_dev, float eps
  */
 MOE_API int moe_forward_launch_count(int E, int k, int T, int d, int I);
 
+/*
+ * ------------------------------------------------------ training the router
+ * The gradients a user needs to train the router (W_r, b_r) and the norm's
+ * gain around frozen MXFP4 experts, next to the forward pass that leaves what
+ * they read: moe_workspace_layout's logits, topk_idx, topk_w and yw, or
+ * moe_route's outputs. Order of a backward pass for the sublayer
+ * out = h + MoE(RMSNorm(h)), given dout [T][d]:
+ *   moe_gate_backward           dlogits from dout and the weighted expert rows
+ *   moe_balance_loss(_backward) the auxiliary loss, added to dlogits
+ *   moe_router_backward         dW_r, db_r and dx = dlogits W_r (+ dx_in)
+ *   moe_rms_norm_backward       dg and dh = dh_in + d/dh of the norm
+ * The gradient that reaches x through the frozen experts is not computed; a
+ * caller that has it passes it as dx_in.
+ *
+ * Shared by these entry points:
+ * - T tokens, E, k and d within the range above (1 <= E <= 256, k <= min(E, 32),
+ *   d a multiple of 32 up to 16384). Arrays whose size is a multiple of T may
+ *   be NULL when T is 0; sums over no tokens are zero.
+ * - token_mask_dev [T] uint8, or NULL: a token whose byte is 0 (padding) is
+ *   left out of every sum and count, and none of its floating-point inputs
+ *   (logits, rows, gradients) changes a result, whatever they hold.
+ * - accumulate (0 or 1): add to the output instead of overwriting it.
+ * - Every sum over tokens has a fixed order: the same call gives the same bits.
+ */
+
+/*
+ * Load-balance and z loss of a batch's router logits, with the per-expert
+ * counts. Over the n live tokens, with p_t = softmax(logits_t) over all E:
+ *   f_e = counts_e / (n k),  P_e = (1/n) sum_t p_{t,e},
+ *   balance = E sum_e f_e P_e,  z = (1/n) sum_t lse(logits_t)^2,
+ *   loss = balance_coef * balance + z_coef * z.
+ *   logits_dev     [T][E] f32    topk_idx_dev [T][k] i32
+ *   stats_dev      [4]    f32    loss, balance, z, n
+ *   counts_dev     [E]    i32    live (token, slot) pairs of each expert
+ *   mean_probs_dev [E]    f32    P
+ *   lse_dev        [T]    f32    log sum exp of each row (0 for padded tokens)
+ * An index outside 0..E-1 (a dropped pair, say -1) is not counted. A logit of
+ * -inf has probability 0; a row of nothing but -inf adds nothing to P and z
+ * (its lse is -inf) and gets no gradient. NaN and +inf in a live row give NaN.
+ * Sums over tokens: at most a few hundred terms in fp32, their sums in fp64.
+ */
+MOE_API size_t moe_balance_loss_workspace_size(int E, int k, int T);
+MOE_API moe_status moe_balance_loss(const float* logits_dev, const int32_t* topk_idx_dev,
+                                    const uint8_t* token_mask_dev, int E, int k, int T,
+                                    float balance_coef, float z_coef, float* stats_dev,
+                                    int32_t* counts_dev, float* mean_probs_dev, float* lse_dev,
+                                    void* workspace_dev, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of that loss to the logits (the counts are constants):
+ *   dlogits[t,e] (+)= (dloss / n) p_{t,e} (balance_coef E (f_e - sum_e' f_e' p_{t,e'})
+ *                                          + 2 z_coef lse_t)
+ * lse, counts and stats as moe_balance_loss left them (n is stats[3]), the same
+ * mask and coefficients; dloss_dev: one f32, the gradient of the loss itself,
+ * or NULL for 1. dlogits_dev [T][E] f32; rows of padded tokens are set to 0
+ * (left alone with accumulate).
+ */
+MOE_API moe_status moe_balance_loss_backward(const float* logits_dev, const float* lse_dev,
+                                             const int32_t* counts_dev, const float* stats_dev,
+                                             const uint8_t* token_mask_dev, int E, int k, int T,
+                                             float balance_coef, float z_coef,
+                                             const float* dloss_dev, int accumulate,
+                                             float* dlogits_dev, void* stream);
+
+/*
+ * Gradient to the logits through the selected-set softmax and the weighted sum
+ * out_t = sum_j p_j y_j: with A_j = <dout_t, p_j y_j> (fp32),
+ *   dlogits[t, topk_idx_j] (+)= A_j - p_j sum_l A_l,   0 for the other experts.
+ *   dout_dev [T][d] bf16   gradient of the layer's output
+ *   yw_dev   [T*k][d] f32  p-weighted expert rows in pair order t*k+j, as a
+ *                          forward call leaves them (moe_workspace_layout's yw)
+ *   topk_idx_dev [T][k] i32, topk_w_dev [T][k] f32 (p)
+ * p enters only as a factor, so weights that underflowed to 0 are no case of
+ * their own. Pairs whose index lies outside 0..E-1 get no gradient of their
+ * own; an index that a row holds twice collects both.
+ */
+MOE_API moe_status moe_gate_backward(const void* dout_dev, const float* yw_dev,
+                                     const int32_t* topk_idx_dev, const float* topk_w_dev,
+                                     const uint8_t* token_mask_dev, int E, int k, int T, int d,
+                                     int accumulate, float* dlogits_dev, void* stream);
+
+/*
+ * Gradients of the router product s = x W_r^T + b_r:
+ *   dW[e] (+)= sum_t dlogits[t,e] x_t,  db[e] (+)= sum_t dlogits[t,e],
+ *   dx[t] = bf16(sum_e dlogits[t,e] W_r[e] + dx_in[t])     (one rounding)
+ * The rows come as x_dev [T][d] bf16, or (x_dev NULL) are rebuilt from the
+ * checkpoint of moe_rms_norm_checkpoint as q 2^(s-127) rstd_t g: q_dev [T][d]
+ * E4M3, scales_dev [T][d/32] E8M0, rstd_dev [T] f32, g_dev [d] f32 (all four,
+ * or all four NULL).
+ * dW_dev [E][d] f32, db_dev [E] f32, dx_dev [T][d] bf16: each may be NULL (not
+ * computed; without dW no rows are read). dx_in_dev [T][d] bf16 or NULL, may
+ * be dx_dev itself; accumulate concerns dW and db. A padded token's dx row is
+ * its dx_in row (0 without one).
+ */
+MOE_API size_t moe_router_backward_workspace_size(int E, int T, int d);
+MOE_API moe_status moe_router_backward(const float* dlogits_dev, const float* W_r_dev,
+                                       const void* x_dev, const uint8_t* q_dev,
+                                       const uint8_t* scales_dev, const float* rstd_dev,
+                                       const float* g_dev, const uint8_t* token_mask_dev, int E,
+                                       int T, int d, const void* dx_in_dev, int accumulate,
+                                       float* dW_dev, float* db_dev, void* dx_dev,
+                                       void* workspace_dev, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_rms_norm that keeps what its backward pass and moe_router_backward read:
+ * the input rows as an 8-bit checkpoint instead of h and x in bf16 (1.03 bytes
+ * per element instead of 4).
+ *   x_dev [T][d] bf16: as moe_rms_norm, bit for bit; NULL: not written
+ *   q_dev [T][d] E4M3, scales_dev [T][d/32] E8M0: h as moe_mx_quantize with
+ *         MOE_ACT_MXFP8 converts it, byte for byte
+ *   rstd_dev [T] f32: 1 / sqrt(mean(h_t^2) + eps)
+ */
+MOE_API moe_status moe_rms_norm_checkpoint(const void* h_dev, const float* g_dev, float eps, int T,
+                                           int d, void* x_dev, uint8_t* q_dev,
+                                           uint8_t* scales_dev, float* rstd_dev, void* stream);
+
+/*
+ * Backward of the norm, n = h rstd:
+ *   dh[t] = bf16(dh_in[t] + rstd_t (g dx_t - n_t mean(n_t g dx_t)))
+ *   dg    (+)= sum_t dx_t n_t
+ * dx_dev [T][d] bf16; rows h_dev [T][d] bf16, or (h_dev NULL) the checkpoint's
+ * q_dev and scales_dev; dh_in_dev [T][d] bf16 (the residual's gradient) or
+ * NULL. dh_dev [T][d] bf16 may be dx_dev or dh_in_dev; dg_dev [d] f32. A
+ * padded token's dh row is its dh_in row (0 without one).
+ */
+MOE_API size_t moe_rms_norm_backward_workspace_size(int T, int d);
+MOE_API moe_status moe_rms_norm_backward(const void* dx_dev, const void* h_dev,
+                                         const uint8_t* q_dev, const uint8_t* scales_dev,
+                                         const float* rstd_dev, const float* g_dev,
+                                         const uint8_t* token_mask_dev, int T, int d,
+                                         const void* dh_in_dev, int accumulate, void* dh_dev,
+                                         float* dg_dev, void* workspace_dev,
+                                         size_t workspace_bytes, void* stream);
+
+/*
+ * moe_forward_block whose norm also leaves the checkpoint (q_dev, scales_dev,
+ * rstd_dev as moe_rms_norm_checkpoint): the training form of the sublayer.
+ * Same arguments, output bits, errors and launches otherwise; the logits,
+ * choices, weights and weighted rows that the backward pass reads stay in the
+ * workspace (moe_workspace_layout) until its next use.
+ */
+MOE_API moe_status moe_forward_block_checkpoint(
+    const void* h_dev, const float* g_dev, float eps, const float* W_r_dev, const float* b_r_dev,
+    const uint8_t* Wgu_codes_dev, const uint8_t* Wgu_scales_dev, const float* gu_bias_dev,
+    const uint8_t* Wd_codes_dev, const uint8_t* Wd_scales_dev, const float* down_bias_dev, int E,
+    int k, int T, int d, int I, void* out_dev, uint8_t* q_dev, uint8_t* scales_dev,
+    float* rstd_dev, void* workspace_dev, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

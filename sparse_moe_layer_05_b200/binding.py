@@ -32,6 +32,10 @@ EXPORTS = [
     "moe_set_tile_policy", "moe_route_noalloc",
     "moe_workspace_size_block", "moe_forward_block", "moe_rms_norm", "moe_forward_biased",
     "moe_forward_timed_events", "moe_forward_ex", "moe_mx_quantize", "moe_forward_timed_ex",
+    "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_balance_loss_backward",
+    "moe_gate_backward", "moe_router_backward_workspace_size", "moe_router_backward",
+    "moe_rms_norm_checkpoint", "moe_rms_norm_backward_workspace_size", "moe_rms_norm_backward",
+    "moe_forward_block_checkpoint",
 ]
 # the measurement library (libmoe_b200_probe.so, include/moe_b200_probe.h)
 PROBE_EXPORTS = ["moe_probe_tensor_rate", "moe_probe_error_string", "moe_probe_error_site"]
@@ -131,6 +135,28 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.moe_set_tile_policy.argtypes = [i32]
     lib.moe_forward_launch_count.restype = i32
     lib.moe_forward_launch_count.argtypes = [i32] * 5
+    f32 = ctypes.c_float
+    lib.moe_balance_loss_workspace_size.restype = sz
+    lib.moe_balance_loss_workspace_size.argtypes = [i32] * 3
+    lib.moe_balance_loss.restype = i32
+    lib.moe_balance_loss.argtypes = [vp, vp, vp, i32, i32, i32, f32, f32, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_balance_loss_backward.restype = i32
+    lib.moe_balance_loss_backward.argtypes = [vp] * 5 + [i32, i32, i32, f32, f32, vp, i32, vp, vp]
+    lib.moe_gate_backward.restype = i32
+    lib.moe_gate_backward.argtypes = [vp] * 5 + [i32] * 5 + [vp, vp]
+    lib.moe_router_backward_workspace_size.restype = sz
+    lib.moe_router_backward_workspace_size.argtypes = [i32] * 3
+    lib.moe_router_backward.restype = i32
+    lib.moe_router_backward.argtypes = ([vp] * 8 + [i32] * 3 + [vp, i32] + [vp] * 4 + [sz, vp])
+    lib.moe_rms_norm_checkpoint.restype = i32
+    lib.moe_rms_norm_checkpoint.argtypes = [vp, vp, f32, i32, i32, vp, vp, vp, vp, vp]
+    lib.moe_rms_norm_backward_workspace_size.restype = sz
+    lib.moe_rms_norm_backward_workspace_size.argtypes = [i32] * 2
+    lib.moe_rms_norm_backward.restype = i32
+    lib.moe_rms_norm_backward.argtypes = [vp] * 7 + [i32, i32, vp, i32, vp, vp, vp, sz, vp]
+    lib.moe_forward_block_checkpoint.restype = i32
+    lib.moe_forward_block_checkpoint.argtypes = ([vp, fp, f32] + fwd_b[1:15] + [vp, vp, vp]
+                                                 + fwd_b[15:])
     _lib = lib
     return lib
 
@@ -180,6 +206,40 @@ def _require_cuda(*ts) -> None:
             raise ValueError("expected CUDA tensors")
         if t is not None and not t.is_contiguous():
             raise ValueError("expected contiguous tensors")
+
+
+_F32, _F16, _I32, _U8, _E4M3, _E8M0 = "f32", "bf16", "i32", "u8", "e4m3", "e8m0"
+_DTYPES = None
+
+
+def _args(**tensors) -> list:
+    """Pointers of the tensors of a training call, checked: CUDA, one device
+    (the current one), contiguous, and of the type and number of elements that
+    name=(tensor, type, elements) asks for; a None tensor gives a null pointer.
+    Without these checks a wrong size would be read past its end."""
+    import torch
+    global _DTYPES
+    if _DTYPES is None:
+        _DTYPES = {_F32: (torch.float32,), _F16: (torch.bfloat16, torch.uint16),
+                   _I32: (torch.int32,), _U8: (torch.uint8, torch.bool),
+                   _E4M3: (torch.uint8, torch.float8_e4m3fn),
+                   _E8M0: (torch.uint8, torch.float8_e8m0fnu)}
+    cur = torch.cuda.current_device()
+    ptrs = []
+    for name, (t, kind, n) in tensors.items():
+        if t is None:
+            ptrs.append(None)
+            continue
+        if not t.is_cuda or t.get_device() != cur:
+            raise ValueError(f"{name}: expected a tensor on the current CUDA device")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous tensor")
+        if t.dtype not in _DTYPES[kind]:
+            raise ValueError(f"{name}: expected {kind} elements, got {t.dtype}")
+        if t.numel() != n:
+            raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
+        ptrs.append(t.data_ptr())
+    return ptrs
 
 
 # ---------------------------------------------------------------- sizes ----
@@ -359,6 +419,120 @@ def moe_mxfp4_to_bf16(codes, scales, rows: int, K: int, out, stream=None) -> Non
     _require_cuda(codes, scales, out)
     _check("moe_mxfp4_to_bf16", load().moe_mxfp4_to_bf16(
         _ptr(codes), _ptr(scales), rows, K, _ptr(out), _stream(stream)))
+
+
+# ------------------------------------------------- training the router ----
+
+def moe_balance_loss_workspace_size(E: int, k: int, T: int) -> int:
+    return int(load().moe_balance_loss_workspace_size(E, k, T))
+
+
+def moe_router_backward_workspace_size(E: int, T: int, d: int) -> int:
+    return int(load().moe_router_backward_workspace_size(E, T, d))
+
+
+def moe_rms_norm_backward_workspace_size(T: int, d: int) -> int:
+    return int(load().moe_rms_norm_backward_workspace_size(T, d))
+
+
+def moe_balance_loss(logits, topk_idx, E: int, k: int, T: int, balance_coef: float, z_coef: float,
+                     stats, counts, mean_probs, lse, workspace, token_mask=None,
+                     stream=None) -> None:
+    """Load-balance and z loss of logits [T, E] f32 with the per-expert counts:
+    stats f32 [4] (loss, balance, z, live tokens), counts i32 [E], mean_probs
+    f32 [E], lse f32 [T]. token_mask u8 or bool [T]: 0 leaves a token out."""
+    lo, ix, mk, sa, co, mp, ls, ws = _args(
+        logits=(logits, _F32, T * E), topk_idx=(topk_idx, _I32, T * k),
+        token_mask=(token_mask, _U8, T), stats=(stats, _F32, 4), counts=(counts, _I32, E),
+        mean_probs=(mean_probs, _F32, E), lse=(lse, _F32, T),
+        workspace=(workspace, _U8, workspace.numel()))
+    _check("moe_balance_loss", load().moe_balance_loss(
+        lo, ix, mk, E, k, T, balance_coef, z_coef, sa, co, mp, ls, ws, workspace.numel(),
+        _stream(stream)))
+
+
+def moe_balance_loss_backward(logits, lse, counts, stats, E: int, k: int, T: int,
+                              balance_coef: float, z_coef: float, dlogits, dloss=None,
+                              token_mask=None, accumulate: bool = False, stream=None) -> None:
+    """dlogits [T, E] f32 (+)= gradient of moe_balance_loss; dloss f32 [1] on the
+    device (None: 1)."""
+    lo, ls, co, sa, mk, dv, dl = _args(
+        logits=(logits, _F32, T * E), lse=(lse, _F32, T), counts=(counts, _I32, E),
+        stats=(stats, _F32, 4), token_mask=(token_mask, _U8, T), dloss=(dloss, _F32, 1),
+        dlogits=(dlogits, _F32, T * E))
+    _check("moe_balance_loss_backward", load().moe_balance_loss_backward(
+        lo, ls, co, sa, mk, E, k, T, balance_coef, z_coef, dv, int(accumulate), dl,
+        _stream(stream)))
+
+
+def moe_gate_backward(dout, yw, topk_idx, topk_w, E: int, k: int, T: int, d: int, dlogits,
+                      token_mask=None, accumulate: bool = False, stream=None) -> None:
+    """dlogits [T, E] f32 (+)= gradient through the selected-set softmax, from
+    dout bf16 [T, d] and the weighted expert rows yw f32 [T*k, d]."""
+    do, yp, ix, wp, mk, dl = _args(
+        dout=(dout, _F16, T * d), yw=(yw, _F32, T * k * d), topk_idx=(topk_idx, _I32, T * k),
+        topk_w=(topk_w, _F32, T * k), token_mask=(token_mask, _U8, T),
+        dlogits=(dlogits, _F32, T * E))
+    _check("moe_gate_backward", load().moe_gate_backward(
+        do, yp, ix, wp, mk, E, k, T, d, int(accumulate), dl, _stream(stream)))
+
+
+def moe_router_backward(dlogits, W_r, E: int, T: int, d: int, dW, db, dx, workspace, x=None,
+                        q=None, scales=None, rstd=None, g=None, dx_in=None, token_mask=None,
+                        accumulate: bool = False, stream=None) -> None:
+    """dW f32 [E, d], db f32 [E], dx bf16 [T, d] (each may be None) from dlogits
+    f32 [T, E]; the input rows as x bf16 [T, d], or as the checkpoint q, scales,
+    rstd with the norm's gain g."""
+    dl, wr, xp, qp, sp, rp, gp, mk, di, dw, bp, dp, ws = _args(
+        dlogits=(dlogits, _F32, T * E), W_r=(W_r, _F32, E * d), x=(x, _F16, T * d),
+        q=(q, _E4M3, T * d), scales=(scales, _E8M0, T * (d // 32)), rstd=(rstd, _F32, T),
+        g=(g, _F32, d), token_mask=(token_mask, _U8, T), dx_in=(dx_in, _F16, T * d),
+        dW=(dW, _F32, E * d), db=(db, _F32, E), dx=(dx, _F16, T * d),
+        workspace=(workspace, _U8, workspace.numel()))
+    _check("moe_router_backward", load().moe_router_backward(
+        dl, wr, xp, qp, sp, rp, gp, mk, E, T, d, di, int(accumulate), dw, bp, dp, ws,
+        workspace.numel(), _stream(stream)))
+
+
+def moe_rms_norm_checkpoint(h, g, eps: float, T: int, d: int, x, q, scales, rstd,
+                            stream=None) -> None:
+    """moe_rms_norm that also leaves h as an 8-bit checkpoint: q E4M3 [T, d],
+    scales E8M0 [T, d/32], and rstd f32 [T]; x may be None."""
+    hp, gp, xp, qp, sp, rp = _args(
+        h=(h, _F16, T * d), g=(g, _F32, d), x=(x, _F16, T * d), q=(q, _E4M3, T * d),
+        scales=(scales, _E8M0, T * (d // 32)), rstd=(rstd, _F32, T))
+    _check("moe_rms_norm_checkpoint", load().moe_rms_norm_checkpoint(
+        hp, gp, eps, T, d, xp, qp, sp, rp, _stream(stream)))
+
+
+def moe_rms_norm_backward(dx, g, rstd, T: int, d: int, dh, dg, workspace, h=None, q=None,
+                          scales=None, dh_in=None, token_mask=None, accumulate: bool = False,
+                          stream=None) -> None:
+    """dh bf16 [T, d] and dg f32 [d] of the norm, from its bf16 input rows h or
+    their checkpoint q, scales."""
+    dp, hp, qp, sp, rp, gp, mk, di, oh, og, ws = _args(
+        dx=(dx, _F16, T * d), h=(h, _F16, T * d), q=(q, _E4M3, T * d),
+        scales=(scales, _E8M0, T * (d // 32)), rstd=(rstd, _F32, T), g=(g, _F32, d),
+        token_mask=(token_mask, _U8, T), dh_in=(dh_in, _F16, T * d), dh=(dh, _F16, T * d),
+        dg=(dg, _F32, d), workspace=(workspace, _U8, workspace.numel()))
+    _check("moe_rms_norm_backward", load().moe_rms_norm_backward(
+        dp, hp, qp, sp, rp, gp, mk, T, d, di, int(accumulate), oh, og, ws, workspace.numel(),
+        _stream(stream)))
+
+
+def moe_forward_block_checkpoint(h, g, eps: float, W_r, b_r, Wgu_codes, Wgu_scales, Wd_codes,
+                                 Wd_scales, E: int, k: int, T: int, d: int, I: int, out, q, scales,
+                                 rstd, workspace, stream=None, gu_bias=None,
+                                 down_bias=None) -> None:
+    """moe_forward_block that also leaves the norm's 8-bit checkpoint."""
+    _require_cuda(h, g, W_r, b_r, Wgu_codes, Wgu_scales, gu_bias, Wd_codes, Wd_scales, down_bias,
+                  out, workspace)
+    qp, sp, rp = _args(q=(q, _E4M3, T * d), scales=(scales, _E8M0, T * (d // 32)),
+                       rstd=(rstd, _F32, T))
+    _check("moe_forward_block_checkpoint", load().moe_forward_block_checkpoint(
+        _ptr(h), _ptr(g), eps, _ptr(W_r), _ptr(b_r), _ptr(Wgu_codes), _ptr(Wgu_scales),
+        _ptr(gu_bias), _ptr(Wd_codes), _ptr(Wd_scales), _ptr(down_bias), E, k, T, d, I,
+        _ptr(out), qp, sp, rp, _ptr(workspace), workspace.numel(), _stream(stream)))
 
 
 TILE_AUTO, TILE_SINGLE, TILE_PAIR, TILE_SWAP, TILE_MX, TILE_MX_PAIR = 0, 1, 2, 3, 4, 5

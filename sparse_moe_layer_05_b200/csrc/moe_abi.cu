@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/moe_b200.h"
@@ -185,6 +186,11 @@ int* chunk_status(void* ws, const HostioPlan& hp, int c) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool all_aligned16(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!aligned16(p)) return false;
+  return true;
+}
 
 // Device capability and SM count, cached per device.
 moe_status device_info(int* num_sms) {
@@ -559,6 +565,42 @@ moe_status run_forward(const uint16_t* x, const float* W_r, const float* b_r, co
   return MOE_OK;
 }
 
+// The sublayer with its pre-norm and residual; with q, scales and rstd the norm
+// also leaves the 8-bit checkpoint of its input.
+moe_status forward_block(const void* h_dev, const float* g_dev, float eps, const float* W_r_dev,
+                         const float* b_r_dev, const uint8_t* Wgu_codes_dev,
+                         const uint8_t* Wgu_scales_dev, const float* gu_bias_dev,
+                         const uint8_t* Wd_codes_dev, const uint8_t* Wd_scales_dev,
+                         const float* down_bias_dev, int E, int k, int T, int d, int I,
+                         void* out_dev, uint8_t* q, uint8_t* scales, float* rstd,
+                         void* workspace_dev, size_t workspace_bytes, void* stream) {
+  moe_status s = check_forward_args(h_dev, W_r_dev, b_r_dev, Wgu_codes_dev, Wgu_scales_dev,
+                                    Wd_codes_dev, Wd_scales_dev, E, k, T, d, I, out_dev,
+                                    workspace_dev);
+  if (s != MOE_OK) return s;
+  if (!g_dev || !aligned16(g_dev) || !(eps >= 0.f)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(gu_bias_dev) || !aligned16(down_bias_dev)) return MOE_ERR_INVALID_ARG;
+  Layout L;
+  make_layout(E, k, T, d, I, false, &L, true);
+  if (workspace_bytes < L.pub.total) return MOE_ERR_WORKSPACE;
+  if (T == 0) return MOE_OK;
+  int num_sms = 0;
+  if ((s = device_info(&num_sms)) != MOE_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const uint16_t* h = static_cast<const uint16_t*>(h_dev);
+  uint16_t* x = at<uint16_t>(workspace_dev, L.x_norm);
+  if (q)
+    MOE_CUDA(moe::launch_rms_norm_checkpoint(h, g_dev, eps, T, d, x, q, scales, rstd, st));
+  else
+    MOE_CUDA(moe::launch_rms_norm(h, g_dev, eps, T, d, x, st));
+  FwdOpts o = default_opts();
+  o.gu_bias = gu_bias_dev;
+  o.dn_bias = down_bias_dev;
+  return run_forward(x, W_r_dev, b_r_dev, Wgu_codes_dev, Wgu_scales_dev, Wd_codes_dev,
+                     Wd_scales_dev, E, k, T, d, I, static_cast<uint16_t*>(out_dev), workspace_dev,
+                     L, st, num_sms, o, nullptr, h);
+}
+
 }  // namespace
 
 extern "C" {
@@ -697,28 +739,24 @@ moe_status moe_forward_block(const void* h_dev, const float* g_dev, float eps, c
                              const float* down_bias_dev, int E, int k, int T, int d, int I,
                              void* out_dev, void* workspace_dev, size_t workspace_bytes,
                              void* stream) {
-  moe_status s = check_forward_args(h_dev, W_r_dev, b_r_dev, Wgu_codes_dev, Wgu_scales_dev,
-                                    Wd_codes_dev, Wd_scales_dev, E, k, T, d, I, out_dev,
-                                    workspace_dev);
-  if (s != MOE_OK) return s;
-  if (!g_dev || !aligned16(g_dev) || !(eps >= 0.f)) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(gu_bias_dev) || !aligned16(down_bias_dev)) return MOE_ERR_INVALID_ARG;
-  Layout L;
-  make_layout(E, k, T, d, I, false, &L, true);
-  if (workspace_bytes < L.pub.total) return MOE_ERR_WORKSPACE;
-  if (T == 0) return MOE_OK;
-  int num_sms = 0;
-  if ((s = device_info(&num_sms)) != MOE_OK) return s;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const uint16_t* h = static_cast<const uint16_t*>(h_dev);
-  uint16_t* x = at<uint16_t>(workspace_dev, L.x_norm);
-  MOE_CUDA(moe::launch_rms_norm(h, g_dev, eps, T, d, x, st));
-  FwdOpts o = default_opts();
-  o.gu_bias = gu_bias_dev;
-  o.dn_bias = down_bias_dev;
-  return run_forward(x, W_r_dev, b_r_dev, Wgu_codes_dev, Wgu_scales_dev, Wd_codes_dev,
-                     Wd_scales_dev, E, k, T, d, I, static_cast<uint16_t*>(out_dev), workspace_dev,
-                     L, st, num_sms, o, nullptr, h);
+  return forward_block(h_dev, g_dev, eps, W_r_dev, b_r_dev, Wgu_codes_dev, Wgu_scales_dev,
+                       gu_bias_dev, Wd_codes_dev, Wd_scales_dev, down_bias_dev, E, k, T, d, I,
+                       out_dev, nullptr, nullptr, nullptr, workspace_dev, workspace_bytes, stream);
+}
+
+moe_status moe_forward_block_checkpoint(
+    const void* h_dev, const float* g_dev, float eps, const float* W_r_dev, const float* b_r_dev,
+    const uint8_t* Wgu_codes_dev, const uint8_t* Wgu_scales_dev, const float* gu_bias_dev,
+    const uint8_t* Wd_codes_dev, const uint8_t* Wd_scales_dev, const float* down_bias_dev, int E,
+    int k, int T, int d, int I, void* out_dev, uint8_t* q_dev, uint8_t* scales_dev,
+    float* rstd_dev, void* workspace_dev, size_t workspace_bytes, void* stream) {
+  if (!q_dev || !scales_dev || !rstd_dev || !aligned16(q_dev) || !aligned16(scales_dev) ||
+      !aligned16(rstd_dev))
+    return MOE_ERR_INVALID_ARG;
+  return forward_block(h_dev, g_dev, eps, W_r_dev, b_r_dev, Wgu_codes_dev, Wgu_scales_dev,
+                       gu_bias_dev, Wd_codes_dev, Wd_scales_dev, down_bias_dev, E, k, T, d, I,
+                       out_dev, q_dev, scales_dev, rstd_dev, workspace_dev, workspace_bytes,
+                       stream);
 }
 
 moe_status moe_forward_hostio(const void* x_host, const float* W_r_dev, const float* b_r_dev,
@@ -1017,6 +1055,185 @@ moe_status moe_selftest_wait_timeout(void* workspace_dev, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   MOE_CUDA(cudaMemsetAsync(workspace_dev, 0, sizeof(int), st));
   MOE_CUDA(moe::launch_wait_timeout_selftest(static_cast<int*>(workspace_dev), st));
+  return MOE_OK;
+}
+
+// ---------------------------------------------------- training the router ----
+
+size_t moe_balance_loss_workspace_size(int E, int k, int T) {
+  if (!shape_ok(E, k, T, 32)) return 0;
+  return moe::balance_scratch_bytes(E, T);
+}
+
+moe_status moe_balance_loss(const float* logits_dev, const int32_t* topk_idx_dev,
+                            const uint8_t* token_mask_dev, int E, int k, int T, float balance_coef,
+                            float z_coef, float* stats_dev, int32_t* counts_dev,
+                            float* mean_probs_dev, float* lse_dev, void* workspace_dev,
+                            size_t workspace_bytes, void* stream) {
+  if (E < 1 || k < 1 || T < 0) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!logits_dev || !topk_idx_dev || !lse_dev)) return MOE_ERR_INVALID_ARG;
+  if (!stats_dev || !counts_dev || !mean_probs_dev || !workspace_dev) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned16({logits_dev, topk_idx_dev, token_mask_dev, stats_dev, counts_dev,
+                      mean_probs_dev, lse_dev, workspace_dev}))
+    return MOE_ERR_INVALID_ARG;
+  if (!shape_ok(E, k, T, 32)) return MOE_ERR_UNSUPPORTED;
+  if (workspace_bytes < moe::balance_scratch_bytes(E, T)) return MOE_ERR_WORKSPACE;
+  int num_sms = 0;
+  moe_status s = device_info(&num_sms);
+  if (s != MOE_OK) return s;
+  PdlPass pdl_pass;
+  MOE_CUDA(moe::launch_balance_loss(logits_dev, topk_idx_dev, token_mask_dev, E, k, T, balance_coef,
+                                    z_coef, stats_dev, counts_dev, mean_probs_dev, lse_dev,
+                                    workspace_dev, static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_balance_loss_backward(const float* logits_dev, const float* lse_dev,
+                                     const int32_t* counts_dev, const float* stats_dev,
+                                     const uint8_t* token_mask_dev, int E, int k, int T,
+                                     float balance_coef, float z_coef, const float* dloss_dev,
+                                     int accumulate, float* dlogits_dev, void* stream) {
+  if (E < 1 || k < 1 || T < 0 || (accumulate & ~1)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!logits_dev || !lse_dev || !dlogits_dev)) return MOE_ERR_INVALID_ARG;
+  if (!counts_dev || !stats_dev) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned16({logits_dev, lse_dev, counts_dev, stats_dev, token_mask_dev, dlogits_dev}) ||
+      (reinterpret_cast<uintptr_t>(dloss_dev) & 3))
+    return MOE_ERR_INVALID_ARG;
+  if (!shape_ok(E, k, T, 32)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  int num_sms = 0;
+  moe_status s = device_info(&num_sms);
+  if (s != MOE_OK) return s;
+  PdlPass pdl_pass;
+  MOE_CUDA(moe::launch_balance_backward(logits_dev, lse_dev, counts_dev, stats_dev, token_mask_dev, E,
+                                        k, T, balance_coef, z_coef, dloss_dev, accumulate != 0,
+                                        dlogits_dev, static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_gate_backward(const void* dout_dev, const float* yw_dev, const int32_t* topk_idx_dev,
+                             const float* topk_w_dev, const uint8_t* token_mask_dev, int E, int k,
+                             int T, int d, int accumulate, float* dlogits_dev, void* stream) {
+  if (E < 1 || k < 1 || T < 0 || d < 1 || (accumulate & ~1)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!dout_dev || !yw_dev || !topk_idx_dev || !topk_w_dev || !dlogits_dev))
+    return MOE_ERR_INVALID_ARG;
+  if (!all_aligned16({dout_dev, yw_dev, topk_idx_dev, topk_w_dev, token_mask_dev, dlogits_dev}))
+    return MOE_ERR_INVALID_ARG;
+  if (!shape_ok(E, k, T, d)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  int num_sms = 0;
+  moe_status s = device_info(&num_sms);
+  if (s != MOE_OK) return s;
+  PdlPass pdl_pass;
+  MOE_CUDA(moe::launch_gate_backward(static_cast<const uint16_t*>(dout_dev), yw_dev, topk_idx_dev,
+                                     topk_w_dev, token_mask_dev, E, k, T, d, accumulate != 0,
+                                     dlogits_dev, static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+size_t moe_router_backward_workspace_size(int E, int T, int d) {
+  if (!shape_ok(E, 1, T, d)) return 0;
+  return align256(16) + moe::router_grad_scratch_bytes(E, T, d);
+}
+
+moe_status moe_router_backward(const float* dlogits_dev, const float* W_r_dev, const void* x_dev,
+                               const uint8_t* q_dev, const uint8_t* scales_dev,
+                               const float* rstd_dev, const float* g_dev,
+                               const uint8_t* token_mask_dev, int E, int T, int d,
+                               const void* dx_in_dev, int accumulate, float* dW_dev, float* db_dev,
+                               void* dx_dev, void* workspace_dev, size_t workspace_bytes,
+                               void* stream) {
+  if (E < 1 || T < 0 || d < 1 || (accumulate & ~1)) return MOE_ERR_INVALID_ARG;
+  if (!workspace_dev || (!dW_dev && !db_dev && !dx_dev && T > 0)) return MOE_ERR_INVALID_ARG;
+  const bool ckpt = q_dev || scales_dev || rstd_dev || g_dev;
+  if (T > 0) {
+    if (!dlogits_dev || (dx_dev && !W_r_dev) || (x_dev && ckpt)) return MOE_ERR_INVALID_ARG;
+    if (ckpt && (!q_dev || !scales_dev || !rstd_dev || !g_dev)) return MOE_ERR_INVALID_ARG;
+    if (dW_dev && !x_dev && !ckpt) return MOE_ERR_INVALID_ARG;
+    if (dx_in_dev && !dx_dev) return MOE_ERR_INVALID_ARG;
+  }
+  if (!all_aligned16({dlogits_dev, W_r_dev, x_dev, q_dev, scales_dev, rstd_dev, g_dev,
+                      token_mask_dev, dx_in_dev, dW_dev, db_dev, dx_dev, workspace_dev}))
+    return MOE_ERR_INVALID_ARG;
+  if (!shape_ok(E, 1, T, d)) return MOE_ERR_UNSUPPORTED;
+  if (workspace_bytes < moe_router_backward_workspace_size(E, T, d)) return MOE_ERR_WORKSPACE;
+  int num_sms = 0;
+  moe_status s = device_info(&num_sms);
+  if (s != MOE_OK) return s;
+  moe::RouterGradProblem p = {};
+  p.dlogits = dlogits_dev;
+  p.W_r = W_r_dev;
+  p.x = static_cast<const uint16_t*>(x_dev);
+  p.q = q_dev;
+  p.scales = scales_dev;
+  p.rstd = rstd_dev;
+  p.g = g_dev;
+  p.mask = token_mask_dev;
+  p.dx_in = static_cast<const uint16_t*>(dx_in_dev);
+  p.E = E;
+  p.T = T;
+  p.d = d;
+  p.accumulate = accumulate != 0;
+  p.dW = dW_dev;
+  p.db = db_dev;
+  p.dx = static_cast<uint16_t*>(dx_dev);
+  p.status = static_cast<int*>(workspace_dev);
+  p.scratch = at<void>(workspace_dev, align256(16));
+  PdlPass pdl_pass;
+  MOE_CUDA(moe::launch_router_backward(p, num_sms, static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_rms_norm_checkpoint(const void* h_dev, const float* g_dev, float eps, int T, int d,
+                                   void* x_dev, uint8_t* q_dev, uint8_t* scales_dev,
+                                   float* rstd_dev, void* stream) {
+  if (T < 0 || d < 1 || !(eps >= 0.f)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!h_dev || !q_dev || !scales_dev || !rstd_dev || (x_dev && !g_dev)))
+    return MOE_ERR_INVALID_ARG;
+  if (!all_aligned16({h_dev, g_dev, x_dev, q_dev, scales_dev, rstd_dev})) return MOE_ERR_INVALID_ARG;
+  if (!shape_ok(1, 1, T, d)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  int num_sms = 0;
+  moe_status s = device_info(&num_sms);
+  if (s != MOE_OK) return s;
+  PdlPass pdl_pass;
+  MOE_CUDA(moe::launch_rms_norm_checkpoint(static_cast<const uint16_t*>(h_dev), g_dev, eps, T, d,
+                                           static_cast<uint16_t*>(x_dev), q_dev, scales_dev,
+                                           rstd_dev, static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+size_t moe_rms_norm_backward_workspace_size(int T, int d) {
+  if (!shape_ok(1, 1, T, d)) return 0;
+  return moe::rms_norm_backward_scratch_bytes(T, d);
+}
+
+moe_status moe_rms_norm_backward(const void* dx_dev, const void* h_dev, const uint8_t* q_dev,
+                                 const uint8_t* scales_dev, const float* rstd_dev,
+                                 const float* g_dev, const uint8_t* token_mask_dev, int T, int d,
+                                 const void* dh_in_dev, int accumulate, void* dh_dev,
+                                 float* dg_dev, void* workspace_dev, size_t workspace_bytes,
+                                 void* stream) {
+  if (T < 0 || d < 1 || (accumulate & ~1)) return MOE_ERR_INVALID_ARG;
+  if (!g_dev || !dg_dev || !workspace_dev) return MOE_ERR_INVALID_ARG;
+  if (T > 0) {
+    if (!dx_dev || !rstd_dev || !dh_dev) return MOE_ERR_INVALID_ARG;
+    if (h_dev ? (q_dev || scales_dev) : (!q_dev || !scales_dev)) return MOE_ERR_INVALID_ARG;
+  }
+  if (!all_aligned16({dx_dev, h_dev, q_dev, scales_dev, rstd_dev, g_dev, token_mask_dev, dh_in_dev,
+                      dh_dev, dg_dev, workspace_dev}))
+    return MOE_ERR_INVALID_ARG;
+  if (!shape_ok(1, 1, T, d)) return MOE_ERR_UNSUPPORTED;
+  if (workspace_bytes < moe::rms_norm_backward_scratch_bytes(T, d)) return MOE_ERR_WORKSPACE;
+  int num_sms = 0;
+  moe_status s = device_info(&num_sms);
+  if (s != MOE_OK) return s;
+  PdlPass pdl_pass;
+  MOE_CUDA(moe::launch_rms_norm_backward(
+      static_cast<const uint16_t*>(dx_dev), static_cast<const uint16_t*>(h_dev), q_dev, scales_dev,
+      rstd_dev, g_dev, token_mask_dev, T, d, static_cast<const uint16_t*>(dh_in_dev),
+      accumulate != 0, static_cast<uint16_t*>(dh_dev), dg_dev, workspace_dev,
+      static_cast<cudaStream_t>(stream)));
   return MOE_OK;
 }
 

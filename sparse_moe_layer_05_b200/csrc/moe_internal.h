@@ -241,6 +241,57 @@ bool mx_make_bytes_map(CUtensorMap* m, const uint8_t* base, int rank, const cuui
 bool mx_encode_bf16_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
                         const cuuint64_t* strides, const cuuint32_t* box);
 
+// ------------------------------------------------ training the router ----
+// (moe_router_grad.cu, moe_norm_ckpt.cu; formulas at the kernels)
+// Load-balance and z loss of logits [T][E]: stats [4] (loss, balance, z, live
+// tokens), counts [E], mean_probs [E], lse [T]. scratch: balance_scratch_bytes.
+size_t balance_scratch_bytes(int E, int T);
+cudaError_t launch_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask,
+                                int E, int k, int T, float balance_coef, float z_coef,
+                                float* stats, int32_t* counts, float* mean_probs, float* lse,
+                                void* scratch, cudaStream_t st);
+cudaError_t launch_balance_backward(const float* logits, const float* lse, const int32_t* counts,
+                                    const float* stats, const uint8_t* mask, int E, int k, int T,
+                                    float balance_coef, float z_coef, const float* dloss,
+                                    bool accumulate, float* dlogits, cudaStream_t st);
+// Gradient to the logits through the selected-set softmax.
+cudaError_t launch_gate_backward(const uint16_t* dout, const float* yw, const int32_t* topk_idx,
+                                 const float* topk_w, const uint8_t* mask, int E, int k, int T,
+                                 int d, bool accumulate, float* dlogits, cudaStream_t st);
+// Gradients of the router product: dW [E][d], db [E], dx [T][d] (each may be
+// null). Input rows: x bf16, or q/scales/rstd/g (8-bit checkpoint).
+struct RouterGradProblem {
+  const float* dlogits;     // [T][E]
+  const float* W_r;         // [E][d]
+  const uint16_t* x;        // [T][d] bf16, or null
+  const uint8_t* q;         // [T][d] E4M3 (x null)
+  const uint8_t* scales;    // [T][d/32] E8M0
+  const float* rstd;        // [T]
+  const float* g;           // [d]
+  const uint8_t* mask;      // [T] or null
+  const uint16_t* dx_in;    // [T][d] or null (may be dx)
+  int E, T, d;
+  bool accumulate;          // dW and db: add to what is there
+  float* dW;
+  float* db;
+  uint16_t* dx;
+  void* scratch;            // router_grad_scratch_bytes
+  int* status;
+};
+size_t router_grad_scratch_bytes(int E, int T, int d);
+cudaError_t launch_router_backward(const RouterGradProblem& p, int num_sms, cudaStream_t st);
+// RMSNorm leaving the 8-bit checkpoint of its input (x may be null).
+cudaError_t launch_rms_norm_checkpoint(const uint16_t* h, const float* g, float eps, int T, int d,
+                                       uint16_t* x, uint8_t* q, uint8_t* scales, float* rstd,
+                                       cudaStream_t st);
+// Backward of the norm, from bf16 rows (h) or the checkpoint (q, scales).
+size_t rms_norm_backward_scratch_bytes(int T, int d);
+cudaError_t launch_rms_norm_backward(const uint16_t* dx, const uint16_t* h, const uint8_t* q,
+                                     const uint8_t* scales, const float* rstd, const float* g,
+                                     const uint8_t* mask, int T, int d, const uint16_t* dh_in,
+                                     bool accumulate, uint16_t* dh, float* dg, void* scratch,
+                                     cudaStream_t st);
+
 // Debug/self-test: one bounded wait on an mbarrier that nothing completes.
 cudaError_t launch_wait_timeout_selftest(int* status, cudaStream_t st);
 

@@ -58,6 +58,7 @@
 #include <stdint.h>
 
 #include "moe_internal.h"
+#include "moe_mx_convert.cuh"
 #include "moe_ptx.cuh"
 
 namespace moe {
@@ -130,23 +131,14 @@ __device__ __forceinline__ uint32_t split_group32(const float (&v)[32], float am
   return static_cast<uint32_t>(eh + 127);
 }
 
-__device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
-
 // ------------------------------------------- MX conversion (w4a8, w4a4) ----
 // The OCP Microscaling conversion of one group of 32 values: shared scale
 // X = 2^(floor(log2 max|v|) - emax), emax 8 for E4M3 and 2 for E2M1;
 // elements v / X rounded to the nearest element value (ties to even),
 // magnitudes above the largest normal (448, 6) clamped to it. X's exponent is
 // kept in the E8M0 range (at least -127: groups whose max|v| is below
-// 2^(emax - 127) keep that smallest scale); an all-zero group takes X = 1.
-template <int ACT>
-__device__ __forceinline__ int mx_scale_exp(float amax) {
-  constexpr int emax = ACT == ACT_E2M1 ? 2 : 8;
-  if (!(amax > 0.f)) return 0;
-  const int e = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFF) - 127;  // floor(log2)
-  return max(e - emax, -127);
-}
-
+// 2^(emax - 127) keep that smallest scale); an all-zero group takes X = 1
+// (mx_scale_exp, moe_mx_convert.cuh).
 // 32 values -> element codes: E4M3 bytes in w[0..7] (element i in byte i),
 // or E2M1 codes packed two per byte in w[0..3] (element 2i in the low nibble
 // of byte i). Returns the E8M0 scale byte.

@@ -1,0 +1,436 @@
+// moe_router_grad.cu -- the router's training step: the load-balance and z
+// loss with its gradient, the gradient through the selected-set softmax, and
+// the gradients of the router product.
+//
+//   p[t] = softmax(s[t]) over all E experts, n live tokens, c_e pairs routed to
+//   expert e:  f_e = c_e / (n k),  P_e = (1/n) sum_t p[t,e]
+//   L = a E sum_e f_e P_e + b (1/n) sum_t lse(s[t])^2
+//   dL/ds[t,e] = (1/n) p[t,e] (a E (f_e - sum_e' f_e' p[t,e']) + 2 b lse(s[t]))
+//
+//   out_t = sum_j p_j y_j over the selected set:  A_j = <dout_t, p_j y_j>,
+//   dL/ds[t, idx_j] = p_j (dp_j - sum_l p_l dp_l) = A_j - p_j sum_l A_l
+//
+//   s = x W^T + b:  dW = ds^T x,  db = sum_t ds,  dx = ds W
+//
+// ("llm-surgery-dark-arts-gpt-oss-40b-64a8-init", section 2, "Proof": s_i and
+// p_i.) Sums over tokens are taken in a fixed order: results do not change
+// from call to call.
+#include <cuda_bf16.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "moe_internal.h"
+#include "moe_mx_convert.cuh"
+#include "moe_ptx.cuh"
+
+namespace moe {
+namespace {
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
+  return v;
+}
+
+// -------------------------------------------------------- balance loss ----
+
+constexpr int kMaxE = 256;
+constexpr int kBalBlocks = 148;
+
+int balance_blocks(int T) {
+  const int b = (T + 7) / 8;
+  return b < 1 ? 1 : b > kBalBlocks ? kBalBlocks : b;
+}
+
+// Per block: sums over its tokens of p[e] and lse^2, the counts, live tokens.
+struct BalanceScratch {
+  float* p;        // [blocks][E]
+  int32_t* counts; // [blocks][E]
+  double* z;       // [blocks]
+  int32_t* n;      // [blocks]
+};
+
+BalanceScratch balance_scratch(void* base, int E, int blocks) {
+  BalanceScratch s;
+  uint8_t* b = static_cast<uint8_t*>(base);
+  s.z = reinterpret_cast<double*>(b);
+  b += static_cast<size_t>(kBalBlocks) * 8;
+  s.n = reinterpret_cast<int32_t*>(b);
+  b += static_cast<size_t>(kBalBlocks) * 4;
+  s.p = reinterpret_cast<float*>(b);
+  b += static_cast<size_t>(blocks) * E * 4;
+  s.counts = reinterpret_cast<int32_t*>(b);
+  return s;
+}
+
+// One warp per token, lane l holding logits l, l + 32, ...
+__global__ void __launch_bounds__(256) balance_partial_kernel(
+    const float* __restrict__ logits, const int32_t* __restrict__ idx,
+    const uint8_t* __restrict__ mask, int E, int k, int T, float* __restrict__ lse_out,
+    BalanceScratch sc) {
+  pdl_wait_and_trigger();
+  __shared__ float sp[8][kMaxE];
+  __shared__ int sc_cnt[kMaxE];
+  __shared__ double sz[8];
+  __shared__ int sn[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int e = threadIdx.x; e < E; e += 256) sc_cnt[e] = 0;
+  __syncthreads();
+  float acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  double z = 0.0;
+  int n = 0;
+  for (int t = blockIdx.x * 8 + warp; t < T; t += gridDim.x * 8) {
+    if (mask && mask[t] == 0) {
+      if (lane == 0) lse_out[t] = 0.f;
+      continue;
+    }
+    ++n;
+    float v[8];
+    float m = -CUDART_INF_F;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane + 32 * i;
+      v[i] = e < E ? __ldg(logits + (size_t)t * E + e) : -CUDART_INF_F;
+      m = v[i] > m || v[i] != v[i] ? v[i] : m;   // keeps a NaN
+    }
+    bool nan = m != m;
+    nan = __any_sync(0xFFFFFFFFu, nan);
+    m = warp_max(m);
+    float sum = 0.f;
+    const bool none = m == -CUDART_INF_F && !nan;   // every logit is -inf
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = lane + 32 * i < E && !none ? expf(v[i] - m) : 0.f;
+      sum += v[i];
+    }
+    sum = warp_sum(sum);
+    const float l = none ? -CUDART_INF_F : m + logf(sum);
+    const float inv = none ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] += v[i] * inv;
+    if (lane == 0) {
+      lse_out[t] = l;
+      if (!none) z += static_cast<double>(l) * l;
+    }
+    for (int j = lane; j < k; j += 32) {
+      const int e = __ldg(idx + (size_t)t * k + j);
+      if (static_cast<unsigned>(e) < static_cast<unsigned>(E)) atomicAdd(&sc_cnt[e], 1);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sp[warp][lane + 32 * i] = acc[i];
+  if (lane == 0) {
+    sz[warp] = z;
+    sn[warp] = n;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += 256) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += sp[w][e];
+    sc.p[(size_t)blockIdx.x * E + e] = s;
+    sc.counts[(size_t)blockIdx.x * E + e] = sc_cnt[e];
+  }
+  if (threadIdx.x == 0) {
+    double zz = 0.0;
+    int nn = 0;
+    for (int w = 0; w < 8; ++w) {
+      zz += sz[w];
+      nn += sn[w];
+    }
+    sc.z[blockIdx.x] = zz;
+    sc.n[blockIdx.x] = nn;
+  }
+}
+
+__global__ void __launch_bounds__(256) balance_finish_kernel(BalanceScratch sc, int blocks, int E,
+                                                             int k, float balance_coef,
+                                                             float z_coef, float* stats,
+                                                             int32_t* counts, float* mean_probs) {
+  pdl_wait_and_trigger();
+  __shared__ double red[256];
+  __shared__ double s_z;
+  __shared__ int s_n;
+  if (threadIdx.x == 0) {
+    double z = 0.0;
+    int n = 0;
+    for (int b = 0; b < blocks; ++b) {
+      z += sc.z[b];
+      n += sc.n[b];
+    }
+    s_z = z;
+    s_n = n;
+  }
+  __syncthreads();
+  const int n = s_n, e = threadIdx.x;
+  double term = 0.0;
+  if (e < E) {
+    double p = 0.0;
+    int c = 0;
+    for (int b = 0; b < blocks; ++b) {
+      p += sc.p[(size_t)b * E + e];
+      c += sc.counts[(size_t)b * E + e];
+    }
+    const double mean = n > 0 ? p / n : 0.0;
+    counts[e] = c;
+    mean_probs[e] = static_cast<float>(mean);
+    term = n > 0 ? mean * (static_cast<double>(c) / (static_cast<double>(n) * k)) : 0.0;
+  }
+  red[threadIdx.x] = term;
+  __syncthreads();
+  for (int off = 128; off > 0; off >>= 1) {
+    if (threadIdx.x < off) red[threadIdx.x] += red[threadIdx.x + off];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    const double bal = red[0] * E, z = n > 0 ? s_z / n : 0.0;
+    stats[0] = static_cast<float>(balance_coef * bal + z_coef * z);
+    stats[1] = static_cast<float>(bal);
+    stats[2] = static_cast<float>(z);
+    stats[3] = static_cast<float>(n);
+  }
+}
+
+__global__ void __launch_bounds__(256) balance_backward_kernel(
+    const float* __restrict__ logits, const float* __restrict__ lse,
+    const int32_t* __restrict__ counts, const float* __restrict__ stats,
+    const uint8_t* __restrict__ mask, int E, int k, int T, float balance_coef, float z_coef,
+    const float* __restrict__ dloss, bool accumulate, float* dlogits) {
+  pdl_wait_and_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float n = stats[3];
+  const float scale = n > 0.f ? (dloss ? dloss[0] : 1.f) / n : 0.f;
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = lane + 32 * i;
+    f[i] = e < E && n > 0.f ? static_cast<float>(counts[e]) / (n * (float)k) : 0.f;
+  }
+  for (int t = blockIdx.x * 8 + warp; t < T; t += gridDim.x * 8) {
+    const float l = lse[t];
+    const bool live = (!mask || mask[t] != 0) && l != -CUDART_INF_F;
+    float p[8];
+    float fp = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane + 32 * i;
+      p[i] = live && e < E ? expf(__ldg(logits + (size_t)t * E + e) - l) : 0.f;
+      fp = fmaf(f[i], p[i], fp);
+    }
+    fp = warp_sum(fp);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane + 32 * i;
+      if (e >= E) continue;
+      const float v = live ? scale * p[i] * (balance_coef * (float)E * (f[i] - fp) + 2.f * z_coef * l)
+                           : 0.f;
+      float* o = dlogits + (size_t)t * E + e;
+      *o = accumulate ? *o + v : v;
+    }
+  }
+}
+
+// ------------------------------------------------------- gate gradient ----
+// One block per token: warps take the slots in turn, then every expert's
+// logit collects the slots that chose it.
+__global__ void __launch_bounds__(256) gate_backward_kernel(
+    const uint16_t* __restrict__ dout, const float* __restrict__ yw,
+    const int32_t* __restrict__ idx, const float* __restrict__ w,
+    const uint8_t* __restrict__ mask, int E, int k, int d, bool accumulate, float* dlogits) {
+  pdl_wait_and_trigger();
+  __shared__ float A[32];
+  __shared__ int sidx[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = blockIdx.x;
+  const bool live = !mask || mask[t] != 0;
+  if (threadIdx.x < 32) {
+    A[lane] = 0.f;
+    sidx[lane] = lane < k && live ? idx[t * k + lane] : -1;
+  }
+  __syncthreads();
+  if (live) {
+    for (int j = warp; j < k; j += 8) {
+      const float4* y = reinterpret_cast<const float4*>(yw + (t * k + j) * d);
+      const uint2* o = reinterpret_cast<const uint2*>(dout + t * d);
+      float s = 0.f;
+      for (int c = lane; c < d / 4; c += 32) {
+        const float4 a = __ldg(y + c);
+        const uint2 b = __ldg(o + c);
+        s = fmaf(a.x, __uint_as_float(b.x << 16), s);
+        s = fmaf(a.y, __uint_as_float(b.x & 0xFFFF0000u), s);
+        s = fmaf(a.z, __uint_as_float(b.y << 16), s);
+        s = fmaf(a.w, __uint_as_float(b.y & 0xFFFF0000u), s);
+      }
+      s = warp_sum(s);
+      if (lane == 0) A[j] = s;
+    }
+  }
+  __syncthreads();
+  float sum = 0.f;
+  for (int j = 0; j < k; ++j) sum += A[j];
+  for (int e = threadIdx.x; e < E; e += 256) {
+    float v = 0.f;
+    for (int j = 0; j < k; ++j)
+      if (sidx[j] == e) v += A[j] - w[t * k + j] * sum;
+    float* o = dlogits + t * E + e;
+    *o = accumulate ? *o + v : v;
+  }
+}
+
+// ----------------------------------------------------- router gradient ----
+
+// Input row element of token t, column i: x, or q 2^(s - 127) r g.
+struct RouterRows {
+  const uint16_t* x;
+  const uint8_t* q;
+  const uint8_t* scales;
+  const float* rstd;
+  const float* g;
+};
+__device__ __forceinline__ float router_row(const RouterRows& r, int64_t t, int i, int d) {
+  if (r.x) return bf16_bits_to_f32(r.x[t * d + i]);
+  const float2 f = e4m3x2_to_f32x2(r.q[t * d + i]);
+  return f.x * e8m0_to_f32(r.scales[t * (d / 32) + i / 32]) * r.rstd[t] * r.g[i];
+}
+
+// dW: one thread per column and eight experts; sums of 256 tokens at a time.
+__global__ void __launch_bounds__(128) router_dw_kernel(const float* __restrict__ dl, RouterRows rows,
+                                                        const uint8_t* __restrict__ mask, int E,
+                                                        int T, int d, bool accumulate, float* dW) {
+  pdl_wait_and_trigger();
+  const int i = blockIdx.x * 128 + threadIdx.x, e0 = blockIdx.y * 8;
+  if (i >= d) return;
+  float total[8] = {0.f}, part[8] = {0.f};
+  for (int t = 0; t < T; ++t) {
+    if (mask && mask[t] == 0) continue;
+    const float v = router_row(rows, t, i, d);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (e0 + u < E) part[u] = fmaf(__ldg(dl + (int64_t)t * E + e0 + u), v, part[u]);
+    if ((t & 255) == 255) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        total[u] += part[u];
+        part[u] = 0.f;
+      }
+    }
+  }
+  for (int u = 0; u < 8 && e0 + u < E; ++u) {
+    float* o = dW + (int64_t)(e0 + u) * d + i;
+    const float v = total[u] + part[u];
+    *o = accumulate ? *o + v : v;
+  }
+}
+
+__global__ void __launch_bounds__(256) router_db_kernel(const float* __restrict__ dl,
+                                                        const uint8_t* __restrict__ mask, int E,
+                                                        int T, bool accumulate, float* db) {
+  pdl_wait_and_trigger();
+  __shared__ float sh[256];
+  const int e = blockIdx.x;
+  float s = 0.f;
+  for (int t = threadIdx.x; t < T; t += 256)
+    if (!mask || mask[t] != 0) s += __ldg(dl + (int64_t)t * E + e);
+  sh[threadIdx.x] = s;
+  __syncthreads();
+  for (int off = 128; off > 0; off >>= 1) {
+    if (threadIdx.x < off) sh[threadIdx.x] += sh[threadIdx.x + off];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) db[e] = accumulate ? db[e] + sh[0] : sh[0];
+}
+
+__global__ void __launch_bounds__(256) router_dx_kernel(const float* __restrict__ dl,
+                                                        const float* __restrict__ W,
+                                                        const uint8_t* __restrict__ mask, int E,
+                                                        int d, const uint16_t* dx_in, uint16_t* dx) {
+  pdl_wait_and_trigger();
+  const int64_t t = blockIdx.x;
+  const bool live = !mask || mask[t] != 0;
+  for (int i = threadIdx.x * 2; i < d; i += 512) {
+    float a = 0.f, b = 0.f;
+    if (live)
+      for (int e = 0; e < E; ++e) {
+        const float g = __ldg(dl + t * E + e);
+        const float2 w = __ldg(reinterpret_cast<const float2*>(W + (int64_t)e * d + i));
+        a = fmaf(g, w.x, a);
+        b = fmaf(g, w.y, b);
+      }
+    if (dx_in) {
+      const uint32_t r = *reinterpret_cast<const uint32_t*>(dx_in + t * d + i);
+      a += __uint_as_float(r << 16);
+      b += __uint_as_float(r & 0xFFFF0000u);
+    }
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    *reinterpret_cast<__nv_bfloat162*>(dx + t * d + i) = v;
+  }
+}
+
+}  // namespace
+
+size_t balance_scratch_bytes(int E, int T) {
+  return static_cast<size_t>(kBalBlocks) * 12 + static_cast<size_t>(balance_blocks(T)) * E * 8;
+}
+
+cudaError_t launch_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask,
+                                int E, int k, int T, float balance_coef, float z_coef,
+                                float* stats, int32_t* counts, float* mean_probs, float* lse,
+                                void* scratch, cudaStream_t st) {
+  const int blocks = balance_blocks(T);
+  const BalanceScratch sc = balance_scratch(scratch, E, blocks);
+  cudaError_t e = launch_kernel(balance_partial_kernel, dim3(blocks), dim3(256), 0, st, logits,
+                                topk_idx, mask, E, k, T, lse, sc);
+  if (e != cudaSuccess) return e;
+  pdl_launches() = true;
+  return launch_kernel(balance_finish_kernel, dim3(1), dim3(256), 0, st, sc, blocks, E, k,
+                       balance_coef, z_coef, stats, counts, mean_probs);
+}
+
+cudaError_t launch_balance_backward(const float* logits, const float* lse, const int32_t* counts,
+                                    const float* stats, const uint8_t* mask, int E, int k, int T,
+                                    float balance_coef, float z_coef, const float* dloss,
+                                    bool accumulate, float* dlogits, cudaStream_t st) {
+  const int64_t b = (static_cast<int64_t>(T) + 7) / 8;
+  return launch_kernel(balance_backward_kernel, dim3(b < 148 * 8 ? static_cast<int>(b) : 148 * 8),
+                       dim3(256), 0, st, logits, lse, counts, stats, mask, E, k, T, balance_coef,
+                       z_coef, dloss, accumulate, dlogits);
+}
+
+cudaError_t launch_gate_backward(const uint16_t* dout, const float* yw, const int32_t* topk_idx,
+                                 const float* topk_w, const uint8_t* mask, int E, int k, int T,
+                                 int d, bool accumulate, float* dlogits, cudaStream_t st) {
+  return launch_kernel(gate_backward_kernel, dim3(T), dim3(256), 0, st, dout, yw, topk_idx, topk_w,
+                       mask, E, k, d, accumulate, dlogits);
+}
+
+size_t router_grad_scratch_bytes(int E, int T, int d) {
+  (void)E;
+  (void)T;
+  (void)d;
+  return 16;
+}
+
+cudaError_t launch_router_backward(const RouterGradProblem& p, int num_sms, cudaStream_t st) {
+  (void)num_sms;
+  const RouterRows rows{p.x, p.q, p.scales, p.rstd, p.g};
+  cudaError_t e = cudaSuccess;
+  if (p.dW)
+    e = launch_kernel(router_dw_kernel, dim3((p.d + 127) / 128, (p.E + 7) / 8), dim3(128), 0, st,
+                      p.dlogits, rows, p.mask, p.E, p.T, p.d, p.accumulate, p.dW);
+  if (e == cudaSuccess && p.db)
+    e = launch_kernel(router_db_kernel, dim3(p.E), dim3(256), 0, st, p.dlogits, p.mask, p.E, p.T,
+                      p.accumulate, p.db);
+  if (e == cudaSuccess && p.dx && p.T > 0)
+    e = launch_kernel(router_dx_kernel, dim3(p.T), dim3(256), 0, st, p.dlogits, p.W_r, p.mask, p.E,
+                      p.d, p.dx_in, p.dx);
+  return e;
+}
+
+}  // namespace moe
