@@ -1180,7 +1180,7 @@ moe_status moe_router_backward(const float* dlogits_dev, const float* W_r_dev, c
   p.status = static_cast<int*>(workspace_dev);
   p.scratch = at<void>(workspace_dev, align256(16));
   PdlPass pdl_pass;
-  MOE_CUDA(moe::launch_router_backward(p, num_sms, static_cast<cudaStream_t>(stream)));
+  MOE_CUDA(moe::launch_router_backward(p, static_cast<cudaStream_t>(stream)));
   return MOE_OK;
 }
 

@@ -279,7 +279,10 @@ struct RouterGradProblem {
   int* status;
 };
 size_t router_grad_scratch_bytes(int E, int T, int d);
-cudaError_t launch_router_backward(const RouterGradProblem& p, int num_sms, cudaStream_t st);
+cudaError_t launch_router_backward(const RouterGradProblem& p, cudaStream_t st);
+// The same on the tensor cores (moe_router_grad_tc.cu), T >= 1.
+size_t router_grad_tc_scratch_bytes(int E, int T, int d);
+cudaError_t launch_router_backward_tc(const RouterGradProblem& p, cudaStream_t st);
 // RMSNorm leaving the 8-bit checkpoint of its input (x may be null).
 cudaError_t launch_rms_norm_checkpoint(const uint16_t* h, const float* g, float eps, int T, int d,
                                        uint16_t* x, uint8_t* q, uint8_t* scales, float* rstd,

@@ -284,9 +284,14 @@ __global__ void __launch_bounds__(256) gate_backward_kernel(
   }
 }
 
-// ----------------------------------------------------- router gradient ----
+// ------------------------------------------- router gradient, few tokens ----
+// One launch on the CUDA cores for batches whose three outputs take less time
+// than the tensor-core path's four launches. Every block computes 8 rows by 256
+// columns of a product out[r][i] = sum_k A[k][r] B[k][i]: dW (r experts, k
+// tokens, B = x) or dx (r tokens, k experts, B = W); four groups of 64 threads
+// take every fourth k, a thread four columns.
 
-// Input row element of token t, column i: x, or q 2^(s - 127) r g.
+// Four columns of an input row: x, or q 2^(s - 127) r g.
 struct RouterRows {
   const uint16_t* x;
   const uint8_t* q;
@@ -294,84 +299,142 @@ struct RouterRows {
   const float* rstd;
   const float* g;
 };
-__device__ __forceinline__ float router_row(const RouterRows& r, int64_t t, int i, int d) {
-  if (r.x) return bf16_bits_to_f32(r.x[t * d + i]);
-  const float2 f = e4m3x2_to_f32x2(r.q[t * d + i]);
-  return f.x * e8m0_to_f32(r.scales[t * (d / 32) + i / 32]) * r.rstd[t] * r.g[i];
+__device__ __forceinline__ float4 router_row4(const RouterRows& r, int64_t t, int i, int d) {
+  if (r.x) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(r.x + t * d + i));
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
+                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+  }
+  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(r.q + t * d + i));
+  const float s = e8m0_to_f32(__ldg(r.scales + t * (d / 32) + i / 32)), n = __ldg(r.rstd + t);
+  const float2 a = e4m3x2_to_f32x2(w & 0xFFFFu), b = e4m3x2_to_f32x2(w >> 16);
+  const float4 g = __ldg(reinterpret_cast<const float4*>(r.g + i));
+  return make_float4(a.x * s * n * g.x, a.y * s * n * g.y, b.x * s * n * g.z, b.y * s * n * g.w);
 }
 
-// dW: one thread per column and eight experts; sums of 256 tokens at a time.
-__global__ void __launch_bounds__(128) router_dw_kernel(const float* __restrict__ dl, RouterRows rows,
-                                                        const uint8_t* __restrict__ mask, int E,
-                                                        int T, int d, bool accumulate, float* dW) {
-  pdl_wait_and_trigger();
-  const int i = blockIdx.x * 128 + threadIdx.x, e0 = blockIdx.y * 8;
-  if (i >= d) return;
-  float total[8] = {0.f}, part[8] = {0.f};
-  for (int t = 0; t < T; ++t) {
-    if (mask && mask[t] == 0) continue;
-    const float v = router_row(rows, t, i, d);
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (e0 + u < E) part[u] = fmaf(__ldg(dl + (int64_t)t * E + e0 + u), v, part[u]);
-    if ((t & 255) == 255) {
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        total[u] += part[u];
-        part[u] = 0.f;
-      }
-    }
-  }
-  for (int u = 0; u < 8 && e0 + u < E; ++u) {
-    float* o = dW + (int64_t)(e0 + u) * d + i;
-    const float v = total[u] + part[u];
-    *o = accumulate ? *o + v : v;
-  }
-}
+struct SmallArgs {
+  const float* dl;
+  const float* W;
+  RouterRows rows;
+  const uint8_t* mask;
+  int E, T, d, col_blocks, dw_blocks, dx_blocks;
+  bool accumulate;
+  const uint16_t* dx_in;
+  float* dW;
+  float* db;
+  uint16_t* dx;
+  int* status;
+};
 
-__global__ void __launch_bounds__(256) router_db_kernel(const float* __restrict__ dl,
-                                                        const uint8_t* __restrict__ mask, int E,
-                                                        int T, bool accumulate, float* db) {
+constexpr int kChunk = 64;   // k staged at a time
+
+__global__ void __launch_bounds__(256) router_small_kernel(const SmallArgs a) {
   pdl_wait_and_trigger();
-  __shared__ float sh[256];
-  const int e = blockIdx.x;
-  float s = 0.f;
-  for (int t = threadIdx.x; t < T; t += 256)
-    if (!mask || mask[t] != 0) s += __ldg(dl + (int64_t)t * E + e);
-  sh[threadIdx.x] = s;
-  __syncthreads();
-  for (int off = 128; off > 0; off >>= 1) {
-    if (threadIdx.x < off) sh[threadIdx.x] += sh[threadIdx.x + off];
+  __shared__ float4 A[kChunk][2];          // eight rows of A
+  __shared__ uint8_t keep[kChunk];
+  __shared__ float4 part[3][8][64];
+  const int tid = threadIdx.x, grp = tid >> 6, c = tid & 63;
+  int blk = blockIdx.x;
+  if (blk == 0 && tid == 0) *a.status = 0;
+  if (blk >= a.dw_blocks + a.dx_blocks) {
+    // db: 32 experts, eight warps over the tokens
+    __shared__ float sums[8][32];
+    const int e = (blk - a.dw_blocks - a.dx_blocks) * 32 + (tid & 31), w = tid >> 5;
+    float s = 0.f;
+    if (e < a.E)
+      for (int t = w; t < a.T; t += 8)
+        if (!a.mask || a.mask[t] != 0) s += __ldg(a.dl + static_cast<int64_t>(t) * a.E + e);
+    sums[w][tid & 31] = s;
     __syncthreads();
+    if (w == 0 && e < a.E) {
+      for (int k = 1; k < 8; ++k) s += sums[k][tid & 31];
+      a.db[e] = a.accumulate ? a.db[e] + s : s;
+    }
+    return;
   }
-  if (threadIdx.x == 0) db[e] = accumulate ? db[e] + sh[0] : sh[0];
+  const bool is_dw = blk < a.dw_blocks;
+  if (!is_dw) blk -= a.dw_blocks;
+  const int i = (blk % a.col_blocks) * 256 + c * 4, r0 = blk / a.col_blocks * 8;
+  const int K = is_dw ? a.T : a.E, R = is_dw ? a.E : a.T;
+  float* Af = reinterpret_cast<float*>(A);
+  float4 acc[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < K; k0 += kChunk) {
+    const int n = K - k0 < kChunk ? K - k0 : kChunk;
+    __syncthreads();
+    for (int v = tid; v < kChunk * 8; v += 256) {
+      const int kk = is_dw ? v >> 3 : v & (kChunk - 1), r = is_dw ? v & 7 : v / kChunk;
+      const int64_t t = is_dw ? k0 + kk : r0 + r;
+      const int e = is_dw ? r0 + r : k0 + kk;
+      const bool live = t < a.T && (!a.mask || a.mask[t] != 0);
+      Af[kk * 8 + r] = live && e < a.E ? __ldg(a.dl + t * a.E + e) : 0.f;
+      if (r == 0) keep[kk] = is_dw ? live : kk < n;
+    }
+    __syncthreads();
+    if (i < a.d) {
+#pragma unroll 4
+      for (int kk = grp; kk < n; kk += 4) {
+        if (!keep[kk]) continue;   // a padded token's row is not read
+        const float4 b = is_dw ? router_row4(a.rows, k0 + kk, i, a.d)
+                               : __ldg(reinterpret_cast<const float4*>(
+                                     a.W + static_cast<int64_t>(k0 + kk) * a.d + i));
+        const float4 lo = A[kk][0], hi = A[kk][1];
+        const float w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          acc[r].x = fmaf(w[r], b.x, acc[r].x);
+          acc[r].y = fmaf(w[r], b.y, acc[r].y);
+          acc[r].z = fmaf(w[r], b.z, acc[r].z);
+          acc[r].w = fmaf(w[r], b.w, acc[r].w);
+        }
+      }
+    }
+  }
+  if (grp > 0)
+#pragma unroll
+    for (int r = 0; r < 8; ++r) part[grp - 1][r][c] = acc[r];
+  __syncthreads();
+  // group q finishes rows q and q + 4
+  if (grp == 0)
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const float4 x = part[0][r][c], y = part[1][r][c], z = part[2][r][c];
+      part[0][r][c] = make_float4(acc[r].x + x.x + (y.x + z.x), acc[r].y + x.y + (y.y + z.y),
+                                  acc[r].z + x.z + (y.z + z.z), acc[r].w + x.w + (y.w + z.w));
+    }
+  __syncthreads();
+  if (i >= a.d) return;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = grp + 4 * h;
+    if (r0 + r >= R) continue;
+    float4 s = part[0][r][c];
+    const int64_t at = static_cast<int64_t>(r0 + r) * a.d + i;
+    if (is_dw) {
+      float4* o = reinterpret_cast<float4*>(a.dW + at);
+      if (a.accumulate) {
+        const float4 b = *o;
+        s = make_float4(s.x + b.x, s.y + b.y, s.z + b.z, s.w + b.w);
+      }
+      *o = s;
+    } else {
+      if (a.dx_in) {
+        const uint2 v = *reinterpret_cast<const uint2*>(a.dx_in + at);
+        s.x += __uint_as_float(v.x << 16);
+        s.y += __uint_as_float(v.x & 0xFFFF0000u);
+        s.z += __uint_as_float(v.y << 16);
+        s.w += __uint_as_float(v.y & 0xFFFF0000u);
+      }
+      const __nv_bfloat162 p = __floats2bfloat162_rn(s.x, s.y), q = __floats2bfloat162_rn(s.z, s.w);
+      *reinterpret_cast<uint2*>(a.dx + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&p),
+                                                        *reinterpret_cast<const uint32_t*>(&q));
+    }
+  }
 }
 
-__global__ void __launch_bounds__(256) router_dx_kernel(const float* __restrict__ dl,
-                                                        const float* __restrict__ W,
-                                                        const uint8_t* __restrict__ mask, int E,
-                                                        int d, const uint16_t* dx_in, uint16_t* dx) {
-  pdl_wait_and_trigger();
-  const int64_t t = blockIdx.x;
-  const bool live = !mask || mask[t] != 0;
-  for (int i = threadIdx.x * 2; i < d; i += 512) {
-    float a = 0.f, b = 0.f;
-    if (live)
-      for (int e = 0; e < E; ++e) {
-        const float g = __ldg(dl + t * E + e);
-        const float2 w = __ldg(reinterpret_cast<const float2*>(W + (int64_t)e * d + i));
-        a = fmaf(g, w.x, a);
-        b = fmaf(g, w.y, b);
-      }
-    if (dx_in) {
-      const uint32_t r = *reinterpret_cast<const uint32_t*>(dx_in + t * d + i);
-      a += __uint_as_float(r << 16);
-      b += __uint_as_float(r & 0xFFFF0000u);
-    }
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    *reinterpret_cast<__nv_bfloat162*>(dx + t * d + i) = v;
-  }
-}
+// Most tokens of the one-launch path.
+constexpr int kSmallTokens = 128;
 
 }  // namespace
 
@@ -411,26 +474,31 @@ cudaError_t launch_gate_backward(const uint16_t* dout, const float* yw, const in
 }
 
 size_t router_grad_scratch_bytes(int E, int T, int d) {
-  (void)E;
-  (void)T;
-  (void)d;
-  return 16;
+  return T <= kSmallTokens ? 16 : router_grad_tc_scratch_bytes(E, T, d);
 }
 
-cudaError_t launch_router_backward(const RouterGradProblem& p, int num_sms, cudaStream_t st) {
-  (void)num_sms;
-  const RouterRows rows{p.x, p.q, p.scales, p.rstd, p.g};
-  cudaError_t e = cudaSuccess;
-  if (p.dW)
-    e = launch_kernel(router_dw_kernel, dim3((p.d + 127) / 128, (p.E + 7) / 8), dim3(128), 0, st,
-                      p.dlogits, rows, p.mask, p.E, p.T, p.d, p.accumulate, p.dW);
-  if (e == cudaSuccess && p.db)
-    e = launch_kernel(router_db_kernel, dim3(p.E), dim3(256), 0, st, p.dlogits, p.mask, p.E, p.T,
-                      p.accumulate, p.db);
-  if (e == cudaSuccess && p.dx && p.T > 0)
-    e = launch_kernel(router_dx_kernel, dim3(p.T), dim3(256), 0, st, p.dlogits, p.W_r, p.mask, p.E,
-                      p.d, p.dx_in, p.dx);
-  return e;
+cudaError_t launch_router_backward(const RouterGradProblem& p, cudaStream_t st) {
+  if (p.T > kSmallTokens) return launch_router_backward_tc(p, st);
+  SmallArgs a;
+  a.dl = p.dlogits;
+  a.W = p.W_r;
+  a.rows = RouterRows{p.x, p.q, p.scales, p.rstd, p.g};
+  a.mask = p.mask;
+  a.E = p.E;
+  a.T = p.T;
+  a.d = p.d;
+  a.col_blocks = (p.d + 255) / 256;
+  a.dw_blocks = p.dW ? (p.E + 7) / 8 * a.col_blocks : 0;
+  a.dx_blocks = p.dx ? (p.T + 7) / 8 * a.col_blocks : 0;
+  a.accumulate = p.accumulate;
+  a.dx_in = p.dx_in;
+  a.dW = p.dW;
+  a.db = p.db;
+  a.dx = p.dx;
+  a.status = p.status;
+  const int blocks = a.dw_blocks + a.dx_blocks + (p.db ? (p.E + 31) / 32 : 0);
+  if (blocks == 0) return cudaSuccess;
+  return launch_kernel(router_small_kernel, dim3(blocks), dim3(256), 0, st, a);
 }
 
 }  // namespace moe

@@ -1,0 +1,1106 @@
+// moe_router_grad_tc.cu -- gradients of the router product s = x W^T + b:
+//   dW = ds^T x,  db = sum_t ds,  dx = bf16(ds W + dx_in)
+// on the tensor cores (kind::f16, bf16 operands, fp32 accumulators).
+//
+// Precision. x is bf16, or an 8-bit checkpoint row q 2^(s-127) r_t g_i whose
+// q 2^(s-127) has four significant bits: both enter an UMMA exactly, the row's
+// r_t moves to the other operand (ds r_t, one fp32 rounding) and g_i to the sum.
+// The fp32 operands are split into bf16 terms hi, mid, lo, each the rounding of
+// what the ones before leave:
+//   dW  three terms of ds (24 bits: nothing is lost above 2^-126). The tensor
+//       core's accumulator loses up to an fp32 step per addition (a sum over
+//       1365 tokens was off by 1.6e-6 of its norm, one over 512 by 6e-7), so
+//       every kFlush tokens the sums move to registers and start anew
+//   dx  two terms of ds and of W, products hi hi, mid hi and hi mid: off by at
+//       most 3 2^-18 of each product, 2^-7 of what the bf16 output's own
+//       rounding leaves
+// A padded token's terms are zero, and its row of x is zeroed in shared memory
+// (it may hold a NaN).
+//
+// Launches: the terms (with db's partial sums), dW, and dx with the sums of
+// dW's parts. No operand is transposed in memory: tokens are K of the first product
+// (both operands MN-major) and M of the second (ds K-major, W MN-major).
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "moe_internal.h"
+#include "moe_mx_convert.cuh"
+#include "moe_ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kMD = 128;              // d columns of a dW tile (UMMA M)
+constexpr int kMaxStages = 8;
+constexpr int kFlush = 512;           // tokens per accumulation in TMEM
+constexpr int kSplitTokens = 1 << 16; // tokens per running sum in registers: 128 additions
+constexpr int kSmemLimit = 232448 - 1024;
+constexpr int kFixed = 1024;          // barriers, TMEM address, flags
+constexpr int kTermBlocks = 148 * 4;
+
+// ------------------------------------------------------------- the terms ----
+
+// The terms lie in panels of 64 columns, [panel][token][64]: one TMA box takes
+// any number of panels, and a box's rows are one piece of memory.
+struct Plan {
+  int groups;      // experts in one or two groups of at most 128
+  int eg, egp;     // experts of a group, rounded up to 16
+  int accs;        // accumulators of a group: hi, mid, lo, or hi and mid + lo
+  int lo;          // first column of the lo terms (hi at 0, mid at egp)
+  int panels;      // panels of a group's three terms
+  int ep;          // E rounded up to 16
+  int dx_panel;    // first panel of the two terms the dx product reads
+  int all;         // panels in all
+  int bt;          // tokens per stage of the dW kernel
+  int tiles_d, splits, term_blocks;
+};
+
+Plan make_plan(int E, int T, int d, bool scaled, int num_sms) {
+  Plan p;
+  p.groups = E > 128 ? 2 : 1;
+  p.eg = (E + p.groups - 1) / p.groups;
+  p.egp = (p.eg + 15) / 16 * 16;
+  // two sets of accumulators have to fit TMEM's 512 columns; an UMMA's columns
+  // start at a panel
+  p.accs = 6 * p.egp <= 512 ? 3 : 2;
+  p.lo = p.accs == 3 ? 2 * p.egp : (2 * p.egp + 63) / 64 * 64;
+  p.panels = (p.lo + p.egp + 63) / 64;
+  p.ep = (E + 15) / 16 * 16;
+  // one group's hi and mid terms lie next to each other and serve both products,
+  // unless dW's are those of ds r
+  const bool shared = p.groups == 1 && !scaled;
+  p.dx_panel = shared ? 0 : p.groups * p.panels;
+  p.all = p.groups * p.panels + (shared ? 0 : (2 * p.ep + 63) / 64);
+  p.bt = p.panels <= 5 ? 64 : 32;     // at least four stages
+  p.tiles_d = (d + kMD - 1) / kMD;
+  // one CTA per SM, at least 256 tokens each
+  int s = num_sms / (p.tiles_d * p.groups);
+  if (s > T / 256) s = T / 256;
+  const int least = (T + kSplitTokens - 1) / kSplitTokens;
+  if (s < least) s = least;
+  p.splits = s < 1 ? 1 : s;
+  const int64_t tb = (static_cast<int64_t>(T) + 15) / 16;
+  p.term_blocks = tb < kTermBlocks ? (tb < 1 ? 1 : static_cast<int>(tb)) : kTermBlocks;
+  return p;
+}
+
+__device__ __forceinline__ uint32_t pack2(__nv_bfloat16 a, __nv_bfloat16 b) {
+  return __bfloat16_as_ushort(a) | (static_cast<uint32_t>(__bfloat16_as_ushort(b)) << 16);
+}
+
+struct Terms {
+  __nv_bfloat16 hi, mid, lo;
+};
+__device__ __forceinline__ Terms split3(float v) {
+  Terms t;
+  t.hi = __float2bfloat16_rn(v);
+  const float r = v - __bfloat162float(t.hi);
+  t.mid = __float2bfloat16_rn(r);
+  t.lo = __float2bfloat16_rn(r - __bfloat162float(t.mid));
+  return t;
+}
+
+// Rows [t0, t1) of the terms per block; a thread holds one pair of experts, so
+// its sum for db stays in registers. Blocks sum consecutive tokens.
+constexpr int kTermRows = 4;          // rows a thread loads at a time
+
+__global__ void __launch_bounds__(256) router_terms_kernel(const float* __restrict__ dl,
+                                                           const float* __restrict__ rstd,
+                                                           const uint8_t* __restrict__ mask, int E,
+                                                           int T, const Plan p, int lanes,
+                                                           uint16_t* __restrict__ terms,
+                                                           float* __restrict__ db_part, int* status) {
+  pdl_wait_and_trigger();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
+  __shared__ float2 sum[256];
+  const int64_t t0 = static_cast<int64_t>(T) * blockIdx.x / gridDim.x;
+  const int64_t t1 = static_cast<int64_t>(T) * (blockIdx.x + 1) / gridDim.x;
+  const int pair = threadIdx.x % lanes, row = threadIdx.x / lanes, rows = 256 / lanes;
+  const int e = 2 * pair;
+  const bool even = (E & 1) == 0;
+  const size_t panel = static_cast<size_t>(T) * 64;
+  // address of column c for token 0
+  auto column = [&](int first, int c) { return terms + (first + (c >> 6)) * panel + (c & 63); };
+  float sa = 0.f, sb = 0.f;
+  if (e < p.ep) {
+    const bool together = p.groups == 1;
+    // the pair's places among dW's columns (a group may start at an odd expert)
+    const int ga = e / p.eg, gb = (e + 1) / p.eg, ca = e - ga * p.eg, cb = e + 1 - gb * p.eg;
+    uint16_t* const hi_a = column(together ? 0 : ga * p.panels, together ? e : ca);
+    uint16_t* const mid_a = column(together ? 0 : ga * p.panels, p.egp + (together ? e : ca));
+    uint16_t* const lo_a = column(together ? 0 : ga * p.panels, p.lo + (together ? e : ca));
+    uint16_t* const hi_b = column(gb * p.panels, cb);
+    uint16_t* const mid_b = column(gb * p.panels, p.egp + cb);
+    uint16_t* const lo_b = column(gb * p.panels, p.lo + cb);
+    uint16_t* const hi_x = column(p.dx_panel, e);
+    uint16_t* const mid_x = column(p.dx_panel, p.ep + e);
+    for (int64_t base = t0 + row; base < t1; base += rows * kTermRows) {
+      float a[kTermRows], b[kTermRows], r[kTermRows];
+#pragma unroll
+      for (int k = 0; k < kTermRows; ++k) {
+        const int64_t t = base + k * rows;
+        a[k] = b[k] = 0.f;
+        r[k] = 1.f;
+        if (t < t1 && e < E && (mask == nullptr || mask[t] != 0)) {
+          if (even) {
+            const float2 v = __ldg(reinterpret_cast<const float2*>(dl + t * E + e));
+            a[k] = v.x;
+            b[k] = v.y;
+          } else {
+            a[k] = __ldg(dl + t * E + e);
+            if (e + 1 < E) b[k] = __ldg(dl + t * E + e + 1);
+          }
+          if (rstd) r[k] = __ldg(rstd + t);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kTermRows; ++k) {
+        const int64_t t = base + k * rows;
+        if (t >= t1) continue;
+        const size_t at = static_cast<size_t>(t) * 64;
+        sa += a[k];
+        sb += b[k];
+        Terms u = split3(a[k]), v = split3(b[k]);
+        if (p.dx_panel) {
+          *reinterpret_cast<uint32_t*>(hi_x + at) = pack2(u.hi, v.hi);
+          *reinterpret_cast<uint32_t*>(mid_x + at) = pack2(u.mid, v.mid);
+          if (rstd) {
+            u = split3(a[k] * r[k]);
+            v = split3(b[k] * r[k]);
+          }
+        }
+        if (together) {
+          *reinterpret_cast<uint32_t*>(hi_a + at) = pack2(u.hi, v.hi);
+          *reinterpret_cast<uint32_t*>(mid_a + at) = pack2(u.mid, v.mid);
+          *reinterpret_cast<uint32_t*>(lo_a + at) = pack2(u.lo, v.lo);
+        } else {
+          if (e < E) {
+            hi_a[at] = __bfloat16_as_ushort(u.hi);
+            mid_a[at] = __bfloat16_as_ushort(u.mid);
+            lo_a[at] = __bfloat16_as_ushort(u.lo);
+          }
+          if (e + 1 < E) {
+            hi_b[at] = __bfloat16_as_ushort(v.hi);
+            mid_b[at] = __bfloat16_as_ushort(v.mid);
+            lo_b[at] = __bfloat16_as_ushort(v.lo);
+          }
+        }
+      }
+    }
+  }
+  sum[threadIdx.x] = make_float2(sa, sb);
+  __syncthreads();
+  if (row == 0 && e < E) {
+    for (int r = 1; r < rows; ++r) {
+      const float2 v = sum[r * lanes + pair];
+      sa += v.x;
+      sb += v.y;
+    }
+    db_part[static_cast<size_t>(blockIdx.x) * E + e] = sa;
+    if (e + 1 < E) db_part[static_cast<size_t>(blockIdx.x) * E + e + 1] = sb;
+  }
+}
+
+// ---------------------------------------------------------- descriptors ----
+
+// Shared-memory descriptor of an MN-major operand in the 128-byte swizzled
+// layout: rows of K hold 64 MN elements (128 bytes), 8 rows 1024 bytes apart,
+// the next 64 MN elements `mn_stride` bytes on. 16 of K are 2048 bytes.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t mn_stride) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(mn_stride >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+constexpr uint32_t kAMnMajor = 1u << 15, kBMnMajor = 1u << 16;
+
+// True in one lane of a converged warp, the same lane each time. Instructions
+// that take their operands from uniform registers (UMMAs, TMA) are issued under
+// it from warp-uniform loops: from a loop that one lane runs alone, each took
+// over 100 cycles.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "elect.sync _|P, 0xFFFFFFFF;\n\t"
+      "selp.b32 %0, 1, 0, P;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+// mbar_wait by a whole warp, the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int* status) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, status));
+}
+
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > kWaitLimitNs) return;
+}
+
+// A descriptor's start address may be advanced by adding bytes / 16 (the sums
+// stay within its 14 bits: shared memory ends below 2^18). One thread issues
+// all of a CTA's UMMAs, and rebuilding both descriptors for each took it longer
+// (about 200 cycles) than the tensor core needs for one.
+__device__ __forceinline__ uint64_t advance(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
+
+__device__ __forceinline__ void tma_load_panels(uint32_t dst, const CUtensorMap* m, int token, int panel,
+                                                uint32_t bar) {
+  tma_load_3d(dst, m, 0, token, panel, bar);
+}
+
+// Four E4M3 codes times the scale 2^(s - 127) as two bf16 pairs, exactly. A code
+// placed in bf16 bits as sign | exponent and mantissa << 4 is 2^-120 of its
+// value, subnormal codes included; `m1` and `m2` are bf16 pairs whose product is
+// 2^(s - 7). NaN codes are left to the converting instruction.
+__device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t w, uint32_t m1, uint32_t m2) {
+  const uint32_t p = __byte_perm(w, 0, 0x1404), q = __byte_perm(w, 0, 0x3424);
+  uint32_t a = (p & 0x80008000u) | ((p >> 4) & 0x07F007F0u);
+  uint32_t b = (q & 0x80008000u) | ((q >> 4) & 0x07F007F0u);
+  a = bf16x2_mul(bf16x2_mul(a, m1), m2);
+  b = bf16x2_mul(bf16x2_mul(b, m1), m2);
+  if (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) {
+    if ((w & 0x7Fu) == 0x7Fu) a |= 0x7FFFu;
+    if ((w & 0x7F00u) == 0x7F00u) a |= 0x7FFF0000u;
+    if ((w & 0x7F0000u) == 0x7F0000u) b |= 0x7FFFu;
+    if ((w & 0x7F000000u) == 0x7F000000u) b |= 0x7FFF0000u;
+  }
+  return make_uint2(a, b);
+}
+__device__ __forceinline__ void scale_factors(uint32_t s, uint32_t* m1, uint32_t* m2) {
+  // 2^(s - 7) = 2^c 2^(s - 7 - c), both within bf16's normal range
+  const int c = s > 134u ? 127 : static_cast<int>(s) - 7;
+  const int r = static_cast<int>(s) - 7 - c;
+  const uint32_t a = static_cast<uint32_t>(c + 127) << 7, b = static_cast<uint32_t>(r + 127) << 7;
+  *m1 = s == 255u ? 0x7FC07FC0u : a | (a << 16);
+  *m2 = b | (b << 16);
+}
+
+// ----------------------------------------------------------------- dW ----
+
+struct DwArgs {
+  const uint8_t* mask;
+  const uint8_t* q;
+  const uint8_t* scales;
+  int E, T, d;
+  Plan p;
+  int stages, stage_bytes, tmem_cols;
+  float* part;     // [splits][E][d]
+  int* status;
+};
+
+// Warp 0 loads the stages (TMA), warps 1 and 2 issue the UMMAs: a commit and
+// the wait for the next stage take an issuer some 300 cycles, so the two take
+// stages in turn, each with its own accumulators. Warp 3 zeroes the rows of
+// padded tokens (bf16 rows), warps 4..11 move the accumulators to registers
+// (warp w the lanes of quarter w % 4, chunks of 16 experts in turn with warp
+// w +- 4); 8-bit rows are converted into the stages by warps 12..19.
+constexpr int kSumWarps = 8, kConvWarps = 8;
+constexpr int kSumChunks = 4;         // chunks of 16 experts a warp sums
+constexpr int kPrefetch = 4;          // pieces of 8-bit rows a thread holds in registers
+
+template <bool Q8>
+__global__ void __launch_bounds__(128 + 32 * (kSumWarps + (Q8 ? kConvWarps : 0)), 1)
+    router_dw_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmD,
+                     const DwArgs a) {
+  pdl_wait_and_trigger();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x) >> 5, 0);
+  const int lane = threadIdx.x & 31;
+  const int S = a.stages, BT = a.p.bt;
+  const uint32_t xhalf = static_cast<uint32_t>(BT) * 128;   // 64 columns of a stage's rows
+  uint8_t* fixed = smem + S * a.stage_bytes;
+  const uint32_t bar0 = smem_u32(fixed);
+  auto bar_full = [&](int s) { return bar0 + 8u * s; };
+  auto bar_ready = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
+  auto bar_empty = [&](int s) { return bar0 + 8u * (2 * kMaxStages + s); };
+  auto bar_acc = [&](int b) { return bar0 + 8u * (3 * kMaxStages + b); };
+  auto bar_free = [&](int b) { return bar0 + 8u * (3 * kMaxStages + 2 + b); };
+  uint32_t* misc = reinterpret_cast<uint32_t*>(fixed + 8 * (3 * kMaxStages + 4));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+
+  const int tile = blockIdx.x % a.p.tiles_d;
+  const int group = blockIdx.x / a.p.tiles_d % a.p.groups;
+  const int split = blockIdx.x / (a.p.tiles_d * a.p.groups);
+  const int i0 = tile * kMD;
+  const int nblk = (a.T + BT - 1) / BT;
+  const int b0 = static_cast<int>(static_cast<int64_t>(nblk) * split / a.p.splits);
+  const int b1 = static_cast<int>(static_cast<int64_t>(nblk) * (split + 1) / a.p.splits);
+  const int n = b1 - b0, per = kFlush / BT;
+  // accumulations of the even and the odd stages: they end in turn
+  const int flushes = ((n + 1) / 2 + per - 1) / per + (n / 2 + per - 1) / per;
+  const bool fix = !Q8 && a.mask != nullptr;
+  const bool second = Q8 || fix;        // a stage is complete with bar_ready too
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    misc[2] = misc[3] = misc[4] = 0;
+    for (int s = 0; s < S; ++s) {
+      mbar_init(bar_full(s), 1);
+      mbar_init(bar_ready(s), Q8 ? kConvWarps : 1);
+      mbar_init(bar_empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar_acc(b), 1);
+      mbar_init(bar_free(b), kSumWarps);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&tmD);
+    if (!Q8) tma_prefetch_desc(&tmX);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(misc), static_cast<uint32_t>(a.tmem_cols));
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+
+  if (warp == 0) {
+    int s = 0, ph = 0, issued = 0;
+    for (int i = 0; i < n; ++i) {
+      if (!warp_wait(bar_empty(s), ph ^ 1, abort_flag, a.status)) break;
+      const uint32_t st = sbase + s * a.stage_bytes, bar = bar_full(s);
+      const int t = (b0 + i) * BT;
+      if (elect_one()) {
+        mbar_expect_tx(bar, static_cast<uint32_t>(a.p.panels + (Q8 ? 0 : 2)) * xhalf);
+        if (!Q8) {
+          tma_load_2d(st, &tmX, i0, t, bar);
+          tma_load_2d(st + xhalf, &tmX, i0 + 64, t, bar);
+        }
+        tma_load_panels(st + 2 * xhalf, &tmD, t, group * a.p.panels, bar);
+      }
+      __syncwarp();
+      issued = i + 1;
+      if (++s == S) { s = 0; ph ^= 1; }
+    }
+    if (lane == 0) misc[2] = static_cast<uint32_t>(issued);
+  } else if (warp < 3) {
+    const uint32_t egp = static_cast<uint32_t>(a.p.egp), set = egp * a.p.accs;
+    const uint32_t major = kAMnMajor | kBMnMajor;
+    const uint32_t idesc = idesc_bf16_f32(kMD, static_cast<int>(set)) | major;
+    const uint32_t idesc_lo = idesc_bf16_f32(kMD, static_cast<int>(egp)) | major;
+    const uint64_t a0 = sdesc_mn_sw128(sbase, xhalf), d0 = advance(a0, 2 * xhalf);
+    const uint32_t lo_bytes = static_cast<uint32_t>(a.p.lo) / 64 * xhalf;
+    const bool two = a.p.accs == 2;
+    // issuer w: stages w, w + 2, ... into accumulator set w
+    const int w = warp - 1;
+    const uint32_t acc = tmem + w * set;
+    int consumed = 0, f = 0, at = 0;
+    for (int i = w; i < n; i += 2) {
+      const int s = i % S, ph = i / S & 1;
+      if (at == 0 && !warp_wait(bar_free(w), (f & 1) ^ 1, abort_flag, a.status)) break;
+      if (!warp_wait(bar_full(s), ph, abort_flag, a.status)) break;
+      if (second && !warp_wait(bar_ready(s), ph, abort_flag, a.status)) break;
+      consumed = i + 1;
+      tc_fence_after();
+      uint64_t ad = advance(a0, static_cast<uint32_t>(s * a.stage_bytes));
+      uint64_t bd = advance(d0, static_cast<uint32_t>(s * a.stage_bytes));
+      const bool last = ++at == per || i + 2 >= n;
+      if (elect_one()) {
+        uint32_t on = at != 1;
+        for (int kk = 0; kk < BT / 16; kk += 2) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            umma_bf16(acc, advance(ad, u * 2048), advance(bd, u * 2048), idesc, on | (u != 0));
+            if (two)
+              umma_bf16(acc + egp, advance(ad, u * 2048), advance(bd, lo_bytes + u * 2048), idesc_lo, 1u);
+          }
+          on = 1;
+          ad = advance(ad, 2 * 2048);
+          bd = advance(bd, 2 * 2048);
+        }
+        umma_commit(bar_empty(s));
+        if (last) umma_commit(bar_acc(w));
+      }
+      __syncwarp();
+      if (last) {
+        ++f;
+        at = 0;
+      }
+    }
+    if (lane == 0) misc[3 + w] = static_cast<uint32_t>(consumed);
+  } else if (warp == 3) {
+    if (fix) {
+      int s = 0, ph = 0;
+      for (int i = 0; i < n; ++i) {
+        uint32_t dead[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {   // rows past T are zero already
+          const int64_t t = static_cast<int64_t>(b0 + i) * BT + 32 * h + lane;
+          dead[h] = __ballot_sync(0xFFFFFFFFu, 32 * h < BT && t < a.T && a.mask[t] == 0);
+        }
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_full(s), ph, abort_flag, a.status))) break;
+        uint8_t* half = smem + s * a.stage_bytes + (lane >> 4) * xhalf + (lane & 15) * 8;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          for (uint32_t m = dead[h]; m; m &= m - 1)
+            *reinterpret_cast<uint2*>(half + (32 * h + __ffs(static_cast<int>(m)) - 1) * 128) =
+                make_uint2(0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_ready(s));
+        if (++s == S) { s = 0; ph ^= 1; }
+      }
+    }
+  } else if (warp < 4 + kSumWarps) {
+    // lane = d column, TMEM columns = experts; acc set f & 1 holds flush f
+    const int quad = warp & 3, half = (warp - 4) >> 2, i = i0 + quad * 32 + lane;
+    const int egp = a.p.egp, chunks = egp / 16;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    float sum[kSumChunks][16];
+#pragma unroll
+    for (int c = 0; c < kSumChunks; ++c)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) sum[c][j] = 0.f;
+    bool ok = true;
+    for (int f = 0; f < flushes && ok; ++f) {
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_acc(f & 1), (f >> 1) & 1, abort_flag, a.status));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + lanes + (f & 1) * egp * a.p.accs;
+#pragma unroll
+      for (int c = 0; c < kSumChunks; ++c) {
+        const int ch = 2 * c + half;
+        if (ch >= chunks) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t u[8], v[8], w[8];
+          const uint32_t at = acc + ch * 16 + h * 8;
+          tmem_ld8x2_sync(at, at + egp, u, v);
+          if (a.p.accs == 3) {
+            tmem_ld8_sync(at + 2 * egp, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w[j]));
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            sum[c][8 * h + j] += __uint_as_float(u[j]) + __uint_as_float(v[j]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_free(f & 1));
+    }
+    const int e0 = group * a.p.eg, ne = a.E - e0 < a.p.eg ? a.E - e0 : a.p.eg;
+    float* out = a.part + (static_cast<size_t>(split) * a.E + e0) * a.d + i;
+    if (ok && i < a.d)
+#pragma unroll
+      for (int c = 0; c < kSumChunks; ++c)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int e = (2 * c + half) * 16 + j;
+          if (e < ne) out[static_cast<size_t>(e) * a.d] = sum[c][j];
+        }
+  } else {
+    // 8-bit rows: a thread takes 16 columns of tokens tr, tr + 32, ... of each
+    // stage, one such piece at a time, kPrefetch pieces ahead
+    const int ct = threadIdx.x - 128 - 32 * kSumWarps, tr = ct >> 3, c = ct & 7;
+    const int col = i0 + c * 16, pieces = BT / 32, total = n * pieces;
+    const bool in = col < a.d;
+    uint4 qb[kPrefetch];
+    uint32_t sb[kPrefetch], mb[kPrefetch];
+    auto load = [&](int x, uint4& q, uint32_t& s, uint32_t& m) {
+      const int64_t t = static_cast<int64_t>(b0) * BT + static_cast<int64_t>(x) * 32 + tr;
+      q = make_uint4(0, 0, 0, 0);
+      s = 127u;
+      m = 1u;
+      if (x < total && in && t < a.T) {
+        // loaded whether or not the token is live, and looked at when the piece's
+        // turn comes: no load waits for another
+        q = __ldg(reinterpret_cast<const uint4*>(a.q + t * a.d + col));
+        s = __ldg(a.scales + t * (a.d / 32) + col / 32);
+        if (a.mask) m = __ldg(a.mask + t);
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < kPrefetch; ++u) load(u, qb[u], sb[u], mb[u]);
+    int s = 0, ph = 0, piece = 0;
+    bool ok = true;
+    // kPrefetch pieces per round: the ring of registers is indexed statically
+    for (int x = 0; x < total && ok; x += kPrefetch) {
+#pragma unroll
+      for (int u = 0; u < kPrefetch; ++u) {
+        if (x + u >= total || !ok) continue;
+        if (piece == 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_empty(s), ph ^ 1, abort_flag, a.status));
+        if (!ok) continue;
+        uint32_t m1, m2;
+        if (mb[u] == 0) {
+          qb[u] = make_uint4(0, 0, 0, 0);
+          sb[u] = 127u;
+        }
+        scale_factors(sb[u], &m1, &m2);
+        const uint2 v0 = e4m3x4_to_bf16(qb[u].x, m1, m2), v1 = e4m3x4_to_bf16(qb[u].y, m1, m2);
+        const uint2 v2 = e4m3x4_to_bf16(qb[u].z, m1, m2), v3 = e4m3x4_to_bf16(qb[u].w, m1, m2);
+        load(x + u + kPrefetch, qb[u], sb[u], mb[u]);
+        const int row = piece * 32 + tr, ch = (c & 3) * 2;
+        uint8_t* xa = smem + s * a.stage_bytes + (c >> 2) * xhalf + row * 128;
+        *reinterpret_cast<uint4*>(xa + ((ch ^ (row & 7)) << 4)) = make_uint4(v0.x, v0.y, v1.x, v1.y);
+        *reinterpret_cast<uint4*>(xa + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(v2.x, v2.y, v3.x, v3.y);
+        if (++piece == pieces) {
+          piece = 0;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_ready(s));
+          if (++s == S) { s = 0; ph ^= 1; }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag && threadIdx.x == 0) {
+    // a wait gave up: the loads in flight land and the issued UMMAs finish before
+    // the memory is given back (each wait here is bounded too)
+    const uint32_t issued = misc[2], done = misc[3] > misc[4] ? misc[3] : misc[4];
+    for (uint32_t i = issued > static_cast<uint32_t>(S) ? issued - S : 0; i < issued; ++i)
+      drain_wait(bar_full(static_cast<int>(i % S)), (i / S) & 1u);
+    for (uint32_t i = done > static_cast<uint32_t>(S) ? done - S : 0; i < done; ++i)
+      drain_wait(bar_empty(static_cast<int>(i % S)), (i / S) & 1u);
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, static_cast<uint32_t>(a.tmem_cols));
+  }
+}
+
+// dW = sum of the parts in order (times g), db = sum of the term blocks' sums.
+struct SumArgs {
+  const float* part;
+  const float* g;        // [d] or null
+  const float* db_part;
+  int splits, term_blocks, E, d, blocks;
+  bool accumulate;
+  float* dW;             // null: not wanted
+  float* db;
+};
+
+__device__ __forceinline__ void router_sums(const SumArgs& a, int blk) {
+  const size_t n4 = a.dW ? static_cast<size_t>(a.E) * a.d / 4 : 0;
+  const size_t stride = static_cast<size_t>(a.blocks) * blockDim.x;
+  for (size_t v = static_cast<size_t>(blk) * blockDim.x + threadIdx.x; v < n4; v += stride) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 6
+    for (int k = 0; k < a.splits; ++k) {
+      const float4 b = __ldg(reinterpret_cast<const float4*>(a.part) + k * n4 + v);
+      s.x += b.x;
+      s.y += b.y;
+      s.z += b.z;
+      s.w += b.w;
+    }
+    if (a.g) {
+      const float4 w = __ldg(reinterpret_cast<const float4*>(a.g) + v % (a.d / 4));
+      s.x *= w.x;
+      s.y *= w.y;
+      s.z *= w.z;
+      s.w *= w.w;
+    }
+    float4* o = reinterpret_cast<float4*>(a.dW) + v;
+    if (a.accumulate) {
+      const float4 b = *o;
+      s.x += b.x;
+      s.y += b.y;
+      s.z += b.z;
+      s.w += b.w;
+    }
+    *o = s;
+  }
+  if (!a.db) return;
+  // db: one warp per expert
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  for (int e = blk * warps + (threadIdx.x >> 5); e < a.E; e += a.blocks * warps) {
+    float s = 0.f;
+    for (int b = lane; b < a.term_blocks; b += 32)
+      s += __ldg(a.db_part + static_cast<size_t>(b) * a.E + e);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+    if (lane == 0) a.db[e] = a.accumulate ? a.db[e] + s : s;
+  }
+}
+
+__global__ void __launch_bounds__(256) router_sums_kernel(const SumArgs a) {
+  pdl_wait_and_trigger();
+  router_sums(a, blockIdx.x);
+}
+
+// ----------------------------------------------------------------- dx ----
+
+constexpr int kTM = 128;              // tokens per tile (UMMA M)
+constexpr int kBoxBytes = kTM * 128;  // 64 term columns of a token tile
+constexpr int kMaxRing = 8, kMaxStaging = 4;
+
+struct DxArgs {
+  const float* W;
+  int E, T, d;
+  Plan p;
+  int n_tile, tiles_n, splits;        // columns per tile, tiles along d, CTAs per tile column
+  int boxes, ring, staging;
+  int off_ring, off_staging, off_fixed;
+  int tmem_cols;
+  bool has_in;
+  int main_blocks;                    // the blocks after these sum dW's parts
+  SumArgs sums;
+  int* status;
+};
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(src), "r"(c0), "r"(c1)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+// One CTA keeps the two terms of W's tile columns in shared memory and takes
+// every splits-th token tile. Warps 0 and 12 load ds terms for warps 1 and 3,
+// which issue the UMMAs of the tiles in turn, each into its own accumulator (a
+// commit and the next wait cost an issuer as long as four UMMAs). Warps 4..11
+// add dx_in and round (two per lane quarter, half of the columns each), warp 2 moves the tiles: a staging
+// buffer receives dx_in by TMA, is updated in place and stored by TMA. The
+// grid's last blocks sum dW's parts meanwhile: the tile columns times their
+// splits leave SMs idle (10 of 148 at d = 2880).
+constexpr int kOutWarps = 8;
+
+constexpr int kDxThreads = 160 + 32 * kOutWarps;
+
+__global__ void __launch_bounds__(kDxThreads, 1)
+    router_dx_kernel(const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmIn,
+                     const __grid_constant__ CUtensorMap tmOut, const DxArgs a) {
+  pdl_wait_and_trigger();
+  if (static_cast<int>(blockIdx.x) >= a.main_blocks) {
+    router_sums(a.sums, static_cast<int>(blockIdx.x) - a.main_blocks);
+    return;
+  }
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x) >> 5, 0);
+  const int lane = threadIdx.x & 31;
+  uint8_t* fixed = smem + a.off_fixed;
+  const uint32_t bar0 = smem_u32(fixed);
+  auto bar_full = [&](int s) { return bar0 + 8u * s; };
+  auto bar_empty = [&](int s) { return bar0 + 8u * (kMaxRing + s); };
+  auto bar_acc = [&](int b) { return bar0 + 8u * (2 * kMaxRing + b); };
+  auto bar_free = [&](int b) { return bar0 + 8u * (2 * kMaxRing + 2 + b); };
+  auto bar_in = [&](int s) { return bar0 + 8u * (2 * kMaxRing + 4 + s); };
+  auto bar_out = [&](int s) { return bar0 + 8u * (2 * kMaxRing + 4 + kMaxStaging + s); };
+  uint32_t* misc = reinterpret_cast<uint32_t*>(fixed + 8 * (2 * kMaxRing + 4 + 2 * kMaxStaging));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+
+  const int nt = blockIdx.x % a.tiles_n, split = blockIdx.x / a.tiles_n;
+  const int i0 = nt * a.n_tile;
+  const int ttiles = (a.T + kTM - 1) / kTM;
+  const int n = split < ttiles ? (ttiles - 1 - split) / a.splits + 1 : 0;
+  auto tile_row = [&](int j) { return (split + j * a.splits) * kTM; };
+  const int blocks_n = a.n_tile / 64;                  // 64-column blocks of a tile
+  const int staging_bytes = blocks_n * kTM * 128;
+  const uint32_t wblock = static_cast<uint32_t>(a.p.ep) * 256;   // 2 ep rows of 128 bytes
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 2; i < 7; ++i) misc[i] = 0;
+    for (int s = 0; s < a.ring; ++s) {
+      mbar_init(bar_full(s), 1);
+      mbar_init(bar_empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar_acc(b), 1);
+      mbar_init(bar_free(b), kOutWarps);
+    }
+    for (int s = 0; s < a.staging; ++s) {
+      mbar_init(bar_in(s), 1);
+      mbar_init(bar_out(s), kOutWarps);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&tmD);
+    tma_prefetch_desc(&tmOut);
+    if (a.has_in) tma_prefetch_desc(&tmIn);
+  }
+  if (warp == 3) {
+    tmem_alloc(smem_u32(misc), static_cast<uint32_t>(a.tmem_cols));
+    tmem_relinquish();
+  }
+  // W's columns i0 .. i0 + n_tile - 1 as hi rows 0 .. ep - 1, mid rows ep .. 2 ep - 1
+  const int chunks = a.n_tile / 8;
+#pragma unroll 3
+  for (int v = threadIdx.x; v < a.p.ep * chunks; v += kDxThreads) {
+    const int e = v / chunks, ch = v % chunks, i = i0 + ch * 8;
+    float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (e < a.E && i < a.d) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(a.W + static_cast<size_t>(e) * a.d + i));
+      const float4 y = __ldg(reinterpret_cast<const float4*>(a.W + static_cast<size_t>(e) * a.d + i) + 1);
+      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+      w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+    }
+    uint32_t hi[4], mid[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const Terms p = split3(w[2 * j]), q = split3(w[2 * j + 1]);
+      hi[j] = pack2(p.hi, q.hi);
+      mid[j] = pack2(p.mid, q.mid);
+    }
+    uint8_t* blk = smem + (ch >> 3) * wblock;
+    const uint32_t at = ((ch & 7) ^ (e & 7)) << 4;     // ep is a multiple of 8
+    *reinterpret_cast<uint4*>(blk + e * 128 + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(blk + (a.p.ep + e) * 128 + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+
+  // issuer b has tiles b, b + 2, ..., accumulator b and its half of the ring, so
+  // that a buffer's phases all belong to one loader and one issuer
+  const int half_ring = a.ring / 2;
+  if (warp == 0 || warp == 4 + kOutWarps) {
+    const int b = warp != 0;
+    int k = 0;
+    bool ok = true;
+    for (int j = b; j < n && ok; j += 2)
+      for (int x = 0; x < a.boxes; ++x, ++k) {
+        const int s = b * half_ring + k % half_ring;
+        if (!(ok = warp_wait(bar_empty(s), (k / half_ring & 1) ^ 1, abort_flag, a.status))) break;
+        if (elect_one()) {
+          mbar_expect_tx(bar_full(s), kBoxBytes);
+          tma_load_panels(sbase + a.off_ring + s * kBoxBytes, &tmD, tile_row(j), a.p.dx_panel + x,
+                          bar_full(s));
+        }
+        __syncwarp();
+      }
+    if (lane == 0) misc[2 + b] = static_cast<uint32_t>(k);
+  } else if (warp == 1 || warp == 3) {
+    const uint32_t idesc = idesc_bf16_f32(kTM, a.n_tile) | kBMnMajor;
+    const int steps = a.p.ep / 16;                     // K steps of a term
+    const uint64_t a0 = sdesc_k_sw128(sbase + a.off_ring), w0 = sdesc_mn_sw128(sbase, wblock);
+    const int b = warp >> 1;
+    const uint32_t acc = tmem + b * a.n_tile;
+    int k = 0;
+    bool ok = true;
+    for (int j = b; j < n && ok; j += 2) {
+      if (!(ok = warp_wait(bar_free(b), ((j >> 1) & 1) ^ 1, abort_flag, a.status))) break;
+      tc_fence_after();
+      int step = 0;                                    // ds's hi steps, then its mid steps
+      for (int x = 0; x < a.boxes; ++x) {
+        const int s = b * half_ring + k % half_ring;
+        if (!(ok = warp_wait(bar_full(s), k / half_ring & 1, abort_flag, a.status))) break;
+        ++k;
+        tc_fence_after();
+        const uint64_t ad = advance(a0, static_cast<uint32_t>(s * kBoxBytes));
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const int st = step + kk;
+            if (st >= 2 * steps) break;
+            const bool mid = st >= steps;
+            const uint64_t wd = advance(w0, static_cast<uint32_t>(mid ? st - steps : st) * 2048);
+            umma_bf16(acc, advance(ad, kk * 32), wd, idesc, st != 0);
+            if (!mid) umma_bf16(acc, advance(ad, kk * 32), advance(wd, wblock / 2), idesc, 1u);
+          }
+          umma_commit(bar_empty(s));
+          if (x + 1 == a.boxes) umma_commit(bar_acc(b));
+        }
+        __syncwarp();
+        step += 4;
+      }
+    }
+    if (lane == 0) misc[4 + b] = static_cast<uint32_t>(k);
+  } else if (warp == 2) {
+    auto hand_out = [&](int j) {                       // the staging buffer of tile j
+      const int s = j % a.staging;
+      if (!a.has_in) {
+        mbar_arrive(bar_in(s));
+        return;
+      }
+      mbar_expect_tx(bar_in(s), static_cast<uint32_t>(staging_bytes));
+      for (int k = 0; k < blocks_n; ++k)
+        tma_load_2d(sbase + a.off_staging + s * staging_bytes + k * (kTM * 128), &tmIn, i0 + k * 64,
+                    tile_row(j), bar_in(s));
+    };
+    int out = n < a.staging ? n : a.staging;           // tiles whose buffer was handed out
+    if (elect_one())
+      for (int j = 0; j < out; ++j) hand_out(j);
+    __syncwarp();
+    for (int j = 0; j < n; ++j) {
+      const int s = j % a.staging;
+      if (!warp_wait(bar_out(s), (j / a.staging) & 1, abort_flag, a.status)) break;
+      const bool more = j > 0 && out < n;
+      if (elect_one()) {
+        for (int k = 0; k < blocks_n; ++k)
+          if (i0 + k * 64 < a.d)
+            tma_store_2d(&tmOut, sbase + a.off_staging + s * staging_bytes + k * (kTM * 128),
+                         i0 + k * 64, tile_row(j));
+        bulk_commit();
+        bulk_wait_read<1>();                           // tile j - 1 has left its buffer
+        if (more) hand_out(out);
+      }
+      __syncwarp();
+      out += more;
+    }
+    if (elect_one()) bulk_wait_read<0>();              // the lane that issued the stores
+    __syncwarp();
+    if (lane == 0) misc[6] = static_cast<uint32_t>(out);
+  } else if (warp < 4 + kOutWarps) {
+    const int quad = warp & 3, half = (warp - 4) >> 2, r = quad * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const int c0 = half * (a.n_tile / 2), c1 = c0 + a.n_tile / 2;
+    for (int j = 0; j < n; ++j) {
+      const int b = j & 1, s = j % a.staging;
+      bool ok = mbar_wait(bar_acc(b), (j >> 1) & 1, abort_flag, a.status);
+      ok = ok && mbar_wait(bar_in(s), (j / a.staging) & 1, abort_flag, a.status);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      tc_fence_after();
+      uint8_t* row = smem + a.off_staging + s * staging_bytes + r * 128;
+#pragma unroll 2
+      for (int c = c0; c < c1; c += 16) {
+        uint32_t v[16];
+        tmem_ld16_sync(tmem + b * a.n_tile + lanes + c, v);
+        uint8_t* blk = row + (c >> 6) * (kTM * 128);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint4* o = reinterpret_cast<uint4*>(blk + (((((c & 63) >> 3) + h) ^ (r & 7)) << 4));
+          float f[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v[8 * h + k]);
+          if (a.has_in) {
+            const uint4 w4 = *o;
+            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              f[2 * k] += __uint_as_float(w[k] << 16);
+              f[2 * k + 1] += __uint_as_float(w[k] & 0xFFFF0000u);
+            }
+          }
+          uint32_t p[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const __nv_bfloat162 z = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+            p[k] = *reinterpret_cast<const uint32_t*>(&z);
+          }
+          *o = make_uint4(p[0], p[1], p[2], p[3]);
+        }
+      }
+      tc_fence_before();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar_free(b));
+        mbar_arrive(bar_out(s));
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag && threadIdx.x == 0) {
+    // a wait gave up: loads in flight and issued UMMAs finish first (bounded)
+    const int G = a.staging;
+    for (int b = 0; b < 2; ++b) {
+      const int issued = static_cast<int>(misc[2 + b]), done = static_cast<int>(misc[4 + b]);
+      for (int k = issued > half_ring ? issued - half_ring : 0; k < issued; ++k)
+        drain_wait(bar_full(b * half_ring + k % half_ring), k / half_ring & 1);
+      for (int k = done > half_ring ? done - half_ring : 0; k < done; ++k)
+        drain_wait(bar_empty(b * half_ring + k % half_ring), k / half_ring & 1);
+    }
+    const int out = static_cast<int>(misc[6]);
+    for (int j = out > G ? out - G : 0; j < out; ++j) drain_wait(bar_in(j % G), j / G & 1);
+  }
+  __syncthreads();
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc(tmem, static_cast<uint32_t>(a.tmem_cols));
+  }
+}
+
+int tmem_columns(int need) {
+  int c = 32;
+  while (c < need) c *= 2;
+  return c;
+}
+
+struct Scratch {
+  uint16_t* terms;
+  float* db_part;
+  float* part;
+  size_t bytes;
+};
+
+Scratch scratch_of(void* base, const Plan& p, int E, int T, int d) {
+  Scratch s;
+  uint8_t* b = static_cast<uint8_t*>(base);
+  size_t off = 0;
+  auto take = [&](size_t n) {
+    const size_t o = off;
+    off = (off + n + 255) & ~static_cast<size_t>(255);
+    return o;
+  };
+  const size_t terms = take(static_cast<size_t>(T) * p.all * 128);
+  const size_t db = take(static_cast<size_t>(p.term_blocks) * E * 4);
+  const size_t part = take(static_cast<size_t>(p.splits) * E * d * 4);
+  s.terms = reinterpret_cast<uint16_t*>(b + terms);
+  s.db_part = reinterpret_cast<float*>(b + db);
+  s.part = reinterpret_cast<float*>(b + part);
+  s.bytes = off;
+  return s;
+}
+
+constexpr int kPlanSms = 148;         // the workspace's size goes by the full part
+
+}  // namespace
+
+size_t router_grad_tc_scratch_bytes(int E, int T, int d) {
+  // either form of the rows
+  return scratch_of(nullptr, make_plan(E, T, d, true, kPlanSms), E, T, d).bytes;
+}
+
+template <class K>
+static cudaError_t allow_smem(K kernel, bool (&done)[64]) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  return e;
+}
+
+cudaError_t launch_router_backward_tc(const RouterGradProblem& g, cudaStream_t st) {
+  const bool q8 = g.q != nullptr && g.dW != nullptr;
+  const Plan p = make_plan(g.E, g.T, g.d, q8, kPlanSms);
+  const Scratch sc = scratch_of(g.scratch, p, g.E, g.T, g.d);
+  int lanes = 8;
+  while (2 * lanes < p.ep) lanes *= 2;
+  cudaError_t e = launch_kernel(router_terms_kernel, dim3(p.term_blocks), dim3(256), 0, st, g.dlogits,
+                                q8 ? g.rstd : nullptr, g.mask, g.E, g.T, p, lanes, sc.terms, sc.db_part,
+                                g.status);
+  if (e != cudaSuccess) return e;
+  pdl_launches() = true;
+  auto encode_terms = [&](CUtensorMap* m, const cuuint32_t* box) {
+    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(g.T), static_cast<cuuint64_t>(p.all)};
+    const cuuint64_t strides[2] = {128, static_cast<cuuint64_t>(g.T) * 128};
+    return mx_encode_bf16_map(m, sc.terms, 3, dims, strides, box);
+  };
+  if (g.dW) {
+    DwArgs a;
+    a.mask = g.mask;
+    a.q = g.q;
+    a.scales = g.scales;
+    a.E = g.E;
+    a.T = g.T;
+    a.d = g.d;
+    a.p = p;
+    a.stage_bytes = p.bt * 128 * (2 + p.panels);
+    a.stages = (kSmemLimit - kFixed) / a.stage_bytes;
+    if (a.stages > kMaxStages) a.stages = kMaxStages;
+    // an even number: a stage's buffer always belongs to the same issuer, which has
+    // waited for each of its phases (a parity tells only neighbouring ones apart)
+    a.stages &= ~1;
+    a.tmem_cols = tmem_columns(2 * p.accs * p.egp);
+    a.part = sc.part;
+    a.status = g.status;
+    CUtensorMap tmX = {}, tmD;
+    {
+      const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.bt), static_cast<cuuint32_t>(p.panels)};
+      if (!encode_terms(&tmD, box)) return cudaErrorInvalidValue;
+    }
+    if (!q8) {
+      const cuuint64_t dims[2] = {static_cast<cuuint64_t>(g.d), static_cast<cuuint64_t>(g.T)};
+      const cuuint64_t strides[1] = {static_cast<cuuint64_t>(g.d) * 2};
+      const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(p.bt)};
+      if (!mx_encode_bf16_map(&tmX, g.x, 2, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    static bool done8[64] = {false}, done16[64] = {false};
+    const dim3 grid(p.tiles_d * p.groups * p.splits);
+    const size_t smem = static_cast<size_t>(a.stages) * a.stage_bytes + kFixed + 1024;
+    if (q8) {
+      if ((e = allow_smem(router_dw_kernel<true>, done8)) != cudaSuccess) return e;
+      e = launch_kernel(router_dw_kernel<true>, grid, dim3(128 + 32 * (kSumWarps + kConvWarps)), smem, st, tmX, tmD, a);
+    } else {
+      if ((e = allow_smem(router_dw_kernel<false>, done16)) != cudaSuccess) return e;
+      e = launch_kernel(router_dw_kernel<false>, grid, dim3(128 + 32 * kSumWarps), smem, st, tmX, tmD, a);
+    }
+    if (e != cudaSuccess) return e;
+  }
+  SumArgs sums;
+  sums.part = sc.part;
+  sums.g = q8 ? g.g : nullptr;
+  sums.db_part = sc.db_part;
+  sums.splits = p.splits;
+  sums.term_blocks = p.term_blocks;
+  sums.E = g.E;
+  sums.d = g.d;
+  sums.accumulate = g.accumulate;
+  sums.dW = g.dW;
+  sums.db = g.db;
+  if (g.dx) {
+    DxArgs a;
+    a.W = g.W_r;
+    a.E = g.E;
+    a.T = g.T;
+    a.d = g.d;
+    a.p = p;
+    a.n_tile = p.ep <= 128 ? 128 : 64;
+    a.tiles_n = (g.d + a.n_tile - 1) / a.n_tile;
+    const int ttiles = (g.T + kTM - 1) / kTM;
+    a.splits = kPlanSms / a.tiles_n;
+    if (a.splits > ttiles) a.splits = ttiles;
+    if (a.splits < 1) a.splits = 1;
+    a.boxes = (2 * p.ep + 63) / 64;
+    const int wbytes = p.ep * 256 * (a.n_tile / 64), sbytes = a.n_tile / 64 * kTM * 128;
+    const int room = kSmemLimit - kFixed - wbytes;
+    a.staging = kMaxStaging;
+    while (a.staging > 2 && room - a.staging * sbytes < 6 * kBoxBytes) --a.staging;
+    a.ring = (room - a.staging * sbytes) / kBoxBytes;
+    a.ring = a.ring > kMaxRing ? kMaxRing : a.ring & ~1;
+    a.off_ring = wbytes;
+    a.off_staging = a.off_ring + a.ring * kBoxBytes;
+    a.off_fixed = a.off_staging + a.staging * sbytes;
+    a.tmem_cols = tmem_columns(2 * a.n_tile);
+    a.has_in = g.dx_in != nullptr;
+    a.status = g.status;
+    CUtensorMap tmD, tmIn = {}, tmOut;
+    {
+      const cuuint32_t box[3] = {64, kTM, 1};
+      if (!encode_terms(&tmD, box)) return cudaErrorInvalidValue;
+    }
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(g.d), static_cast<cuuint64_t>(g.T)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(g.d) * 2};
+    const cuuint32_t box[2] = {64, kTM};
+    if (!mx_encode_bf16_map(&tmOut, g.dx, 2, dims, strides, box)) return cudaErrorInvalidValue;
+    if (a.has_in && !mx_encode_bf16_map(&tmIn, g.dx_in, 2, dims, strides, box)) return cudaErrorInvalidValue;
+    static bool done[64] = {false};
+    if ((e = allow_smem(router_dx_kernel, done)) != cudaSuccess) return e;
+    a.main_blocks = a.tiles_n * a.splits;
+    a.sums = sums;
+    a.sums.blocks = 0;
+    if (g.dW || g.db) {
+      const size_t items = g.dW ? static_cast<size_t>(g.E) * g.d / 4 : static_cast<size_t>(g.E) * 32;
+      const size_t most = a.main_blocks < kPlanSms / 2 ? kPlanSms - a.main_blocks : kPlanSms / 2;
+      const size_t want = (items + 2 * kDxThreads - 1) / (2 * kDxThreads);
+      a.sums.blocks = static_cast<int>(want < most ? want : most);
+    }
+    return launch_kernel(router_dx_kernel, dim3(a.main_blocks + a.sums.blocks), dim3(kDxThreads),
+                      static_cast<size_t>(a.off_fixed) + kFixed + 1024, st, tmD, tmIn, tmOut, a);
+  }
+  if (!g.dW && !g.db) return cudaSuccess;
+  const size_t items = g.dW ? static_cast<size_t>(g.E) * g.d / 4 : static_cast<size_t>(g.E) * 32;
+  const size_t want = (items + 255) / 256;
+  sums.blocks = static_cast<int>(want < kPlanSms * 8 ? want : kPlanSms * 8);
+  return launch_kernel(router_sums_kernel, dim3(sums.blocks), dim3(256), 0, st, sums);
+}
+
+}  // namespace moe
