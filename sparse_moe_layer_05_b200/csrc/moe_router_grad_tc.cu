@@ -71,7 +71,8 @@ Plan make_plan(int E, int T, int d, bool scaled, int num_sms) {
   const bool shared = p.groups == 1 && !scaled;
   p.dx_panel = shared ? 0 : p.groups * p.panels;
   p.all = p.groups * p.panels + (shared ? 0 : (2 * p.ep + 63) / 64);
-  p.bt = p.panels <= 5 ? 64 : 32;     // at least four stages
+  // at least four stages fit; 8-bit rows need room as codes too
+  p.bt = p.panels <= (scaled ? 3 : 5) ? 64 : 32;
   p.tiles_d = (d + kMD - 1) / kMD;
   // one CTA per SM, at least 256 tokens each
   int s = num_sms / (p.tiles_d * p.groups);
@@ -100,15 +101,20 @@ __device__ __forceinline__ Terms split3(float v) {
   return t;
 }
 
+// Tokens of a tile's scale words: a stage's words are one aligned piece.
+__host__ __device__ constexpr int64_t padded_tokens(int T) { return (static_cast<int64_t>(T) + 63) / 64 * 64; }
+
 // Rows [t0, t1) of the terms per block; a thread holds one pair of experts, so
 // its sum for db stays in registers. Blocks sum consecutive tokens.
 constexpr int kTermRows = 4;          // rows a thread loads at a time
 
 __global__ void __launch_bounds__(256) router_terms_kernel(const float* __restrict__ dl,
                                                            const float* __restrict__ rstd,
+                                                           const uint8_t* __restrict__ scales,
                                                            const uint8_t* __restrict__ mask, int E,
-                                                           int T, const Plan p, int lanes,
+                                                           int T, int d, const Plan p, int lanes,
                                                            uint16_t* __restrict__ terms,
+                                                           uint16_t* __restrict__ words,
                                                            float* __restrict__ db_part, int* status) {
   pdl_wait_and_trigger();
   if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
@@ -188,6 +194,25 @@ __global__ void __launch_bounds__(256) router_terms_kernel(const float* __restri
       }
     }
   }
+  if (words) {
+    // the 8-bit rows' scales as the dW kernel takes them: [tile of 128 columns]
+    // [token][4] 16-bit words, bit 8 set for a padded token and past the last one
+    const int G = d / 32;
+    const int64_t end = blockIdx.x + 1 == gridDim.x ? padded_tokens(T) : t1;
+    const int64_t items = (end - t0) * p.tiles_d;
+    for (int64_t v = threadIdx.x; v < items; v += 256) {
+      const int tile = static_cast<int>(v % p.tiles_d);
+      const int64_t t = t0 + v / p.tiles_d;
+      const bool row = t < T;
+      const uint32_t dead = !row || (mask && mask[t] == 0) ? 0x100u : 0u;
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = dead | (row && tile * 4 + k < G ? __ldg(scales + t * G + tile * 4 + k) : 127u);
+      reinterpret_cast<uint2*>(words)[tile * static_cast<int64_t>(padded_tokens(T)) + t] =
+          make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+    }
+  }
   sum[threadIdx.x] = make_float2(sa, sb);
   __syncthreads();
   if (row == 0 && e < E) {
@@ -252,39 +277,41 @@ __device__ __forceinline__ void tma_load_panels(uint32_t dst, const CUtensorMap*
   tma_load_3d(dst, m, 0, token, panel, bar);
 }
 
-// Four E4M3 codes times the scale 2^(s - 127) as two bf16 pairs, exactly. A code
-// placed in bf16 bits as sign | exponent and mantissa << 4 is 2^-120 of its
-// value, subnormal codes included; `m1` and `m2` are bf16 pairs whose product is
-// 2^(s - 7). NaN codes are left to the converting instruction.
-__device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t w, uint32_t m1, uint32_t m2) {
-  const uint32_t p = __byte_perm(w, 0, 0x1404), q = __byte_perm(w, 0, 0x3424);
-  uint32_t a = (p & 0x80008000u) | ((p >> 4) & 0x07F007F0u);
-  uint32_t b = (q & 0x80008000u) | ((q >> 4) & 0x07F007F0u);
-  a = bf16x2_mul(bf16x2_mul(a, m1), m2);
-  b = bf16x2_mul(bf16x2_mul(b, m1), m2);
-  if (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) {
-    if ((w & 0x7Fu) == 0x7Fu) a |= 0x7FFFu;
-    if ((w & 0x7F00u) == 0x7F00u) a |= 0x7FFF0000u;
-    if ((w & 0x7F0000u) == 0x7F0000u) b |= 0x7FFFu;
-    if ((w & 0x7F000000u) == 0x7F000000u) b |= 0x7FFF0000u;
+// 16 E4M3 codes times the scale 2^(s - 127) as bf16, exactly. A code placed in
+// bf16 bits as sign | exponent and mantissa << 4 is 2^-120 of its value, subnormal
+// codes included, so one bf16 product with 2^(s - 7) does it (two where that
+// exceeds bf16's range). NaN codes (which only NaN rows have) become NaN.
+__device__ __forceinline__ void e4m3x16_to_bf16(uint4 q, uint32_t s, uint32_t (&o)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  const uint32_t e = s > 134u ? 254u : s + 120u;   // biased exponent of the first factor
+  const uint32_t m = (e << 7) | (e << 23);
+  uint32_t nan = s == 255u ? 0x80u : 0u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t a = __byte_perm(w[k], 0, 0x1404), b = __byte_perm(w[k], 0, 0x3424);
+    o[2 * k] = bf16x2_mul((a & 0x80008000u) | ((a >> 4) & 0x07F007F0u), m);
+    o[2 * k + 1] = bf16x2_mul((b & 0x80008000u) | ((b >> 4) & 0x07F007F0u), m);
+    nan |= ((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
   }
-  return make_uint2(a, b);
-}
-__device__ __forceinline__ void scale_factors(uint32_t s, uint32_t* m1, uint32_t* m2) {
-  // 2^(s - 7) = 2^c 2^(s - 7 - c), both within bf16's normal range
-  const int c = s > 134u ? 127 : static_cast<int>(s) - 7;
-  const int r = static_cast<int>(s) - 7 - c;
-  const uint32_t a = static_cast<uint32_t>(c + 127) << 7, b = static_cast<uint32_t>(r + 127) << 7;
-  *m1 = s == 255u ? 0x7FC07FC0u : a | (a << 16);
-  *m2 = b | (b << 16);
+  if (s > 134u || nan) {
+    const uint32_t r = s > 134u ? s - 134u + 127u : 127u, m2 = (r << 7) | (r << 23);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      o[2 * k] = bf16x2_mul(o[2 * k], m2);
+      o[2 * k + 1] = bf16x2_mul(o[2 * k + 1], m2);
+      if ((w[k] & 0x7Fu) == 0x7Fu || s == 255u) o[2 * k] |= 0x7FFFu;
+      if ((w[k] & 0x7F00u) == 0x7F00u || s == 255u) o[2 * k] |= 0x7FFF0000u;
+      if ((w[k] & 0x7F0000u) == 0x7F0000u || s == 255u) o[2 * k + 1] |= 0x7FFFu;
+      if ((w[k] & 0x7F000000u) == 0x7F000000u || s == 255u) o[2 * k + 1] |= 0x7FFF0000u;
+    }
+  }
 }
 
 // ----------------------------------------------------------------- dW ----
 
 struct DwArgs {
   const uint8_t* mask;
-  const uint8_t* q;
-  const uint8_t* scales;
+  const uint16_t* words;   // the 8-bit rows' scales
   int E, T, d;
   Plan p;
   int stages, stage_bytes, tmem_cols;
@@ -297,24 +324,26 @@ struct DwArgs {
 // stages in turn, each with its own accumulators. Warp 3 zeroes the rows of
 // padded tokens (bf16 rows), warps 4..11 move the accumulators to registers
 // (warp w the lanes of quarter w % 4, chunks of 16 experts in turn with warp
-// w +- 4); 8-bit rows are converted into the stages by warps 12..19.
+// w +- 4). 8-bit rows arrive as codes and scale words and are converted into the
+// stage's bf16 rows by warps 12..15 and 16..19, a stage each in turn. (Rows held in
+// registers ahead of their turn did not work: the loads of the stage after the
+// next were waited for with those of the next, 780 cycles a stage of 32 tokens.)
 constexpr int kSumWarps = 8, kConvWarps = 8;
 constexpr int kSumChunks = 4;         // chunks of 16 experts a warp sums
-constexpr int kPrefetch = 4;          // pieces of 8-bit rows a thread holds in registers
+constexpr int kConvGroup = 4;         // warps that convert a stage
 
-template <bool Q8>
+template <bool Q8, int BT>
 __global__ void __launch_bounds__(128 + 32 * (kSumWarps + (Q8 ? kConvWarps : 0)), 1)
     router_dw_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmD,
                      const DwArgs a) {
-  pdl_wait_and_trigger();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x) >> 5, 0);
   const int lane = threadIdx.x & 31;
-  const int S = a.stages, BT = a.p.bt;
-  const uint32_t xhalf = static_cast<uint32_t>(BT) * 128;   // 64 columns of a stage's rows
+  const int S = a.stages;
+  constexpr uint32_t xhalf = BT * 128;   // 64 columns of a stage's rows
   uint8_t* fixed = smem + S * a.stage_bytes;
   const uint32_t bar0 = smem_u32(fixed);
   auto bar_full = [&](int s) { return bar0 + 8u * s; };
@@ -332,7 +361,8 @@ __global__ void __launch_bounds__(128 + 32 * (kSumWarps + (Q8 ? kConvWarps : 0))
   const int nblk = (a.T + BT - 1) / BT;
   const int b0 = static_cast<int>(static_cast<int64_t>(nblk) * split / a.p.splits);
   const int b1 = static_cast<int>(static_cast<int64_t>(nblk) * (split + 1) / a.p.splits);
-  const int n = b1 - b0, per = kFlush / BT;
+  constexpr int per = kFlush / BT;
+  const int n = b1 - b0;
   // accumulations of the even and the odd stages: they end in turn
   const int flushes = ((n + 1) / 2 + per - 1) / per + (n / 2 + per - 1) / per;
   const bool fix = !Q8 && a.mask != nullptr;
@@ -343,7 +373,7 @@ __global__ void __launch_bounds__(128 + 32 * (kSumWarps + (Q8 ? kConvWarps : 0))
     misc[2] = misc[3] = misc[4] = 0;
     for (int s = 0; s < S; ++s) {
       mbar_init(bar_full(s), 1);
-      mbar_init(bar_ready(s), Q8 ? kConvWarps : 1);
+      mbar_init(bar_ready(s), Q8 ? kConvGroup : 1);
       mbar_init(bar_empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -352,7 +382,7 @@ __global__ void __launch_bounds__(128 + 32 * (kSumWarps + (Q8 ? kConvWarps : 0))
     }
     fence_mbar_init();
     tma_prefetch_desc(&tmD);
-    if (!Q8) tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmX);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(misc), static_cast<uint32_t>(a.tmem_cols));
@@ -361,6 +391,7 @@ __global__ void __launch_bounds__(128 + 32 * (kSumWarps + (Q8 ? kConvWarps : 0))
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait_and_trigger();               // no global memory was touched before
   const uint32_t tmem = misc[0];
 
   if (warp == 0) {
@@ -370,8 +401,13 @@ __global__ void __launch_bounds__(128 + 32 * (kSumWarps + (Q8 ? kConvWarps : 0))
       const uint32_t st = sbase + s * a.stage_bytes, bar = bar_full(s);
       const int t = (b0 + i) * BT;
       if (elect_one()) {
-        mbar_expect_tx(bar, static_cast<uint32_t>(a.p.panels + (Q8 ? 0 : 2)) * xhalf);
-        if (!Q8) {
+        const uint32_t terms = static_cast<uint32_t>(a.p.panels) * xhalf;
+        mbar_expect_tx(bar, terms + (Q8 ? BT * 128 + BT * 8 : 2 * xhalf));
+        if (Q8) {
+          tma_load_2d(st + 2 * xhalf + terms, &tmX, i0, t, bar);
+          bulk_load(st + 2 * xhalf + terms + BT * 128,
+                    a.words + (tile * padded_tokens(a.T) + t) * 4, BT * 8, bar);
+        } else {
           tma_load_2d(st, &tmX, i0, t, bar);
           tma_load_2d(st + xhalf, &tmX, i0 + 64, t, bar);
         }
@@ -401,21 +437,16 @@ __global__ void __launch_bounds__(128 + 32 * (kSumWarps + (Q8 ? kConvWarps : 0))
       if (second && !warp_wait(bar_ready(s), ph, abort_flag, a.status)) break;
       consumed = i + 1;
       tc_fence_after();
-      uint64_t ad = advance(a0, static_cast<uint32_t>(s * a.stage_bytes));
-      uint64_t bd = advance(d0, static_cast<uint32_t>(s * a.stage_bytes));
+      const uint64_t ad = advance(a0, static_cast<uint32_t>(s * a.stage_bytes));
+      const uint64_t bd = advance(d0, static_cast<uint32_t>(s * a.stage_bytes));
       const bool last = ++at == per || i + 2 >= n;
       if (elect_one()) {
-        uint32_t on = at != 1;
-        for (int kk = 0; kk < BT / 16; kk += 2) {
+        const uint32_t on = at != 1;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            umma_bf16(acc, advance(ad, u * 2048), advance(bd, u * 2048), idesc, on | (u != 0));
-            if (two)
-              umma_bf16(acc + egp, advance(ad, u * 2048), advance(bd, lo_bytes + u * 2048), idesc_lo, 1u);
-          }
-          on = 1;
-          ad = advance(ad, 2 * 2048);
-          bd = advance(bd, 2 * 2048);
+        for (int u = 0; u < BT / 16; ++u) {
+          umma_bf16(acc, advance(ad, u * 2048), advance(bd, u * 2048), idesc, on | (u != 0));
+          if (two)
+            umma_bf16(acc + egp, advance(ad, u * 2048), advance(bd, lo_bytes + u * 2048), idesc_lo, 1u);
         }
         umma_commit(bar_empty(s));
         if (last) umma_commit(bar_acc(w));
@@ -431,16 +462,16 @@ __global__ void __launch_bounds__(128 + 32 * (kSumWarps + (Q8 ? kConvWarps : 0))
     if (fix) {
       int s = 0, ph = 0;
       for (int i = 0; i < n; ++i) {
-        uint32_t dead[2];
+        uint32_t dead[BT / 32];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {   // rows past T are zero already
+        for (int h = 0; h < BT / 32; ++h) {   // rows past T are zero already
           const int64_t t = static_cast<int64_t>(b0 + i) * BT + 32 * h + lane;
-          dead[h] = __ballot_sync(0xFFFFFFFFu, 32 * h < BT && t < a.T && a.mask[t] == 0);
+          dead[h] = __ballot_sync(0xFFFFFFFFu, t < a.T && a.mask[t] == 0);
         }
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_full(s), ph, abort_flag, a.status))) break;
         uint8_t* half = smem + s * a.stage_bytes + (lane >> 4) * xhalf + (lane & 15) * 8;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < BT / 32; ++h)
           for (uint32_t m = dead[h]; m; m &= m - 1)
             *reinterpret_cast<uint2*>(half + (32 * h + __ffs(static_cast<int>(m)) - 1) * 128) =
                 make_uint2(0, 0);
@@ -501,58 +532,36 @@ __global__ void __launch_bounds__(128 + 32 * (kSumWarps + (Q8 ? kConvWarps : 0))
           if (e < ne) out[static_cast<size_t>(e) * a.d] = sum[c][j];
         }
   } else {
-    // 8-bit rows: a thread takes 16 columns of tokens tr, tr + 32, ... of each
-    // stage, one such piece at a time, kPrefetch pieces ahead
-    const int ct = threadIdx.x - 128 - 32 * kSumWarps, tr = ct >> 3, c = ct & 7;
-    const int col = i0 + c * 16, pieces = BT / 32, total = n * pieces;
-    const bool in = col < a.d;
-    uint4 qb[kPrefetch];
-    uint32_t sb[kPrefetch], mb[kPrefetch];
-    auto load = [&](int x, uint4& q, uint32_t& s, uint32_t& m) {
-      const int64_t t = static_cast<int64_t>(b0) * BT + static_cast<int64_t>(x) * 32 + tr;
-      q = make_uint4(0, 0, 0, 0);
-      s = 127u;
-      m = 1u;
-      if (x < total && in && t < a.T) {
-        // loaded whether or not the token is live, and looked at when the piece's
-        // turn comes: no load waits for another
-        q = __ldg(reinterpret_cast<const uint4*>(a.q + t * a.d + col));
-        s = __ldg(a.scales + t * (a.d / 32) + col / 32);
-        if (a.mask) m = __ldg(a.mask + t);
-      }
-    };
+    // 8-bit rows: 16 columns of tokens tr, tr + 16, ... of every second stage
+    const int cw = warp - 4 - kSumWarps;
+    const int ct = (cw % kConvGroup) * 32 + lane, tr = ct >> 3, c = ct & 7;
+    for (int i = cw / kConvGroup; i < n; i += 2) {
+      const int s = i % S;
+      if (!warp_wait(bar_full(s), i / S & 1, abort_flag, a.status)) break;
+      uint8_t* const st = smem + s * a.stage_bytes;
+      const uint8_t* const codes = st + (2 + a.p.panels) * xhalf;
+      const uint16_t* const words = reinterpret_cast<const uint16_t*>(codes + BT * 128);
+      uint8_t* const xa = st + (c >> 2) * xhalf;
+      const int ch = (c & 3) * 2;
 #pragma unroll
-    for (int u = 0; u < kPrefetch; ++u) load(u, qb[u], sb[u], mb[u]);
-    int s = 0, ph = 0, piece = 0;
-    bool ok = true;
-    // kPrefetch pieces per round: the ring of registers is indexed statically
-    for (int x = 0; x < total && ok; x += kPrefetch) {
-#pragma unroll
-      for (int u = 0; u < kPrefetch; ++u) {
-        if (x + u >= total || !ok) continue;
-        if (piece == 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_empty(s), ph ^ 1, abort_flag, a.status));
-        if (!ok) continue;
-        uint32_t m1, m2;
-        if (mb[u] == 0) {
-          qb[u] = make_uint4(0, 0, 0, 0);
-          sb[u] = 127u;
+      for (int u = 0; u < BT / 16; ++u) {
+        const int row = 16 * u + tr;
+        uint4 q = *reinterpret_cast<const uint4*>(codes + row * 128 + ((c ^ (row & 7)) << 4));
+        uint32_t w = words[row * 4 + (c >> 1)];
+        if (w > 255u) {      // a padded token's row counts as zeros
+          q = make_uint4(0, 0, 0, 0);
+          w = 127u;
         }
-        scale_factors(sb[u], &m1, &m2);
-        const uint2 v0 = e4m3x4_to_bf16(qb[u].x, m1, m2), v1 = e4m3x4_to_bf16(qb[u].y, m1, m2);
-        const uint2 v2 = e4m3x4_to_bf16(qb[u].z, m1, m2), v3 = e4m3x4_to_bf16(qb[u].w, m1, m2);
-        load(x + u + kPrefetch, qb[u], sb[u], mb[u]);
-        const int row = piece * 32 + tr, ch = (c & 3) * 2;
-        uint8_t* xa = smem + s * a.stage_bytes + (c >> 2) * xhalf + row * 128;
-        *reinterpret_cast<uint4*>(xa + ((ch ^ (row & 7)) << 4)) = make_uint4(v0.x, v0.y, v1.x, v1.y);
-        *reinterpret_cast<uint4*>(xa + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(v2.x, v2.y, v3.x, v3.y);
-        if (++piece == pieces) {
-          piece = 0;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_ready(s));
-          if (++s == S) { s = 0; ph ^= 1; }
-        }
+        uint32_t o[8];
+        e4m3x16_to_bf16(q, w, o);
+        *reinterpret_cast<uint4*>(xa + row * 128 + ((ch ^ (row & 7)) << 4)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(xa + row * 128 + (((ch + 1) ^ (row & 7)) << 4)) =
+            make_uint4(o[4], o[5], o[6], o[7]);
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_ready(s));
     }
   }
   tc_fence_before();
@@ -584,10 +593,11 @@ struct SumArgs {
   float* db;
 };
 
-__device__ __forceinline__ void router_sums(const SumArgs& a, int blk) {
+// The share of block blk's `threads` threads (whole warps), thread tid.
+__device__ __forceinline__ void router_sums(const SumArgs& a, int blk, int tid, int threads) {
   const size_t n4 = a.dW ? static_cast<size_t>(a.E) * a.d / 4 : 0;
-  const size_t stride = static_cast<size_t>(a.blocks) * blockDim.x;
-  for (size_t v = static_cast<size_t>(blk) * blockDim.x + threadIdx.x; v < n4; v += stride) {
+  const size_t stride = static_cast<size_t>(a.blocks) * threads;
+  for (size_t v = static_cast<size_t>(blk) * threads + tid; v < n4; v += stride) {
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 6
     for (int k = 0; k < a.splits; ++k) {
@@ -616,8 +626,8 @@ __device__ __forceinline__ void router_sums(const SumArgs& a, int blk) {
   }
   if (!a.db) return;
   // db: one warp per expert
-  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  for (int e = blk * warps + (threadIdx.x >> 5); e < a.E; e += a.blocks * warps) {
+  const int lane = tid & 31, warps = threads >> 5;
+  for (int e = blk * warps + (tid >> 5); e < a.E; e += a.blocks * warps) {
     float s = 0.f;
     for (int b = lane; b < a.term_blocks; b += 32)
       s += __ldg(a.db_part + static_cast<size_t>(b) * a.E + e);
@@ -629,25 +639,25 @@ __device__ __forceinline__ void router_sums(const SumArgs& a, int blk) {
 
 __global__ void __launch_bounds__(256) router_sums_kernel(const SumArgs a) {
   pdl_wait_and_trigger();
-  router_sums(a, blockIdx.x);
+  router_sums(a, blockIdx.x, threadIdx.x, blockDim.x);
 }
 
 // ----------------------------------------------------------------- dx ----
 
 constexpr int kTM = 128;              // tokens per tile (UMMA M)
 constexpr int kBoxBytes = kTM * 128;  // 64 term columns of a token tile
-constexpr int kMaxRing = 8, kMaxStaging = 4;
+constexpr int kMaxRing = 8, kMaxStaging = 8;
 
 struct DxArgs {
   const float* W;
   int E, T, d;
   Plan p;
-  int n_tile, tiles_n, splits;        // columns per tile, tiles along d, CTAs per tile column
+  int n_tile;                         // columns per tile
+  int full, splits, last_splits;      // whole tiles along d; CTAs per tile, and of the part tile
   int boxes, ring, staging;
   int off_ring, off_staging, off_fixed;
   int tmem_cols;
   bool has_in;
-  int main_blocks;                    // the blocks after these sum dW's parts
   SumArgs sums;
   int* status;
 };
@@ -667,25 +677,26 @@ __device__ __forceinline__ void bulk_wait_read() {
 }
 
 // One CTA keeps the two terms of W's tile columns in shared memory and takes
-// every splits-th token tile. Warps 0 and 12 load ds terms for warps 1 and 3,
-// which issue the UMMAs of the tiles in turn, each into its own accumulator (a
-// commit and the next wait cost an issuer as long as four UMMAs). Warps 4..11
-// add dx_in and round (two per lane quarter, half of the columns each), warp 2 moves the tiles: a staging
-// buffer receives dx_in by TMA, is updated in place and stored by TMA. The
-// grid's last blocks sum dW's parts meanwhile: the tile columns times their
-// splits leave SMs idle (10 of 148 at d = 2880).
+// every splits-th token tile (128 tokens). Warp 0 loads ds terms, warp 1 issues
+// the UMMAs, the tiles into two accumulators in turn (two issuers, one to each
+// accumulator, ran in step and both waited for their outputs at the same time:
+// 2850 cycles a tile where the UMMAs take 1540). A tile leaves in units of 64
+// columns: warps 4..7 and 8..11 (one per lane quarter each) take the units in
+// turn, add dx_in and round; warp 2 moves them: a staging buffer receives dx_in by
+// TMA, is updated in place and stored by TMA (each thread storing its token's
+// columns itself, 32 bytes at a time, took 25 us where this takes 20, T = 8192,
+// E = 32, d = 2880). A store reads its buffer for 1200 cycles under load, so two
+// are in flight. Wide tiles, because ds's terms are read once per tile column:
+// with 128 columns the 128-expert layer's reads (200 MB from L2 at T = 16384) and
+// not the tensor core set the time. Warps 12..15 sum dW's parts meanwhile.
 constexpr int kOutWarps = 8;
-
-constexpr int kDxThreads = 160 + 32 * kOutWarps;
+constexpr int kSumsWarps = 4;
+constexpr int kUnitBytes = kTM * 128;
+constexpr int kDxThreads = 128 + 32 * (kOutWarps + kSumsWarps);
 
 __global__ void __launch_bounds__(kDxThreads, 1)
     router_dx_kernel(const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmIn,
                      const __grid_constant__ CUtensorMap tmOut, const DxArgs a) {
-  pdl_wait_and_trigger();
-  if (static_cast<int>(blockIdx.x) >= a.main_blocks) {
-    router_sums(a.sums, static_cast<int>(blockIdx.x) - a.main_blocks);
-    return;
-  }
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -703,29 +714,34 @@ __global__ void __launch_bounds__(kDxThreads, 1)
   uint32_t* misc = reinterpret_cast<uint32_t*>(fixed + 8 * (2 * kMaxRing + 4 + 2 * kMaxStaging));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
 
-  const int nt = blockIdx.x % a.tiles_n, split = blockIdx.x / a.tiles_n;
+  // CTAs of the whole tiles first, then those of the part tile
+  const bool whole = static_cast<int>(blockIdx.x) < a.full * a.splits;
+  const int nt = whole ? static_cast<int>(blockIdx.x) % a.full : a.full;
+  const int split = whole ? static_cast<int>(blockIdx.x) / a.full
+                          : static_cast<int>(blockIdx.x) - a.full * a.splits;
+  const int splits = whole ? a.splits : a.last_splits;
   const int i0 = nt * a.n_tile;
+  const int units = whole ? a.n_tile / 64 : (a.d - i0 + 63) / 64;   // of a tile
+  const int cols = units * 64;
   const int ttiles = (a.T + kTM - 1) / kTM;
-  const int n = split < ttiles ? (ttiles - 1 - split) / a.splits + 1 : 0;
-  auto tile_row = [&](int j) { return (split + j * a.splits) * kTM; };
-  const int blocks_n = a.n_tile / 64;                  // 64-column blocks of a tile
-  const int staging_bytes = blocks_n * kTM * 128;
+  const int n = split < ttiles ? (ttiles - 1 - split) / splits + 1 : 0;
+  auto tile_row = [&](int j) { return (split + j * splits) * kTM; };
   const uint32_t wblock = static_cast<uint32_t>(a.p.ep) * 256;   // 2 ep rows of 128 bytes
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int i = 2; i < 7; ++i) misc[i] = 0;
+    misc[2] = misc[3] = misc[4] = 0;
     for (int s = 0; s < a.ring; ++s) {
       mbar_init(bar_full(s), 1);
       mbar_init(bar_empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar_acc(b), 1);
-      mbar_init(bar_free(b), kOutWarps);
+      mbar_init(bar_free(b), units > 1 ? kOutWarps : kOutWarps / 2);
     }
     for (int s = 0; s < a.staging; ++s) {
       mbar_init(bar_in(s), 1);
-      mbar_init(bar_out(s), kOutWarps);
+      mbar_init(bar_out(s), kOutWarps / 2);
     }
     fence_mbar_init();
     tma_prefetch_desc(&tmD);
@@ -736,8 +752,8 @@ __global__ void __launch_bounds__(kDxThreads, 1)
     tmem_alloc(smem_u32(misc), static_cast<uint32_t>(a.tmem_cols));
     tmem_relinquish();
   }
-  // W's columns i0 .. i0 + n_tile - 1 as hi rows 0 .. ep - 1, mid rows ep .. 2 ep - 1
-  const int chunks = a.n_tile / 8;
+  // W's columns i0 .. i0 + cols - 1 as hi rows 0 .. ep - 1, mid rows ep .. 2 ep - 1
+  const int chunks = cols / 8;
 #pragma unroll 3
   for (int v = threadIdx.x; v < a.p.ep * chunks; v += kDxThreads) {
     const int e = v / chunks, ch = v % chunks, i = i0 + ch * 8;
@@ -764,43 +780,42 @@ __global__ void __launch_bounds__(kDxThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // W alone was read before the wait: this launch follows one of its own pass,
+  // which began after everything before the pass, W's writer included, had ended
+  pdl_wait_and_trigger();
   const uint32_t tmem = misc[0];
 
-  // issuer b has tiles b, b + 2, ..., accumulator b and its half of the ring, so
-  // that a buffer's phases all belong to one loader and one issuer
-  const int half_ring = a.ring / 2;
-  if (warp == 0 || warp == 4 + kOutWarps) {
-    const int b = warp != 0;
-    int k = 0;
+  if (warp == 0) {
+    int s = 0, ph = 0, issued = 0;
     bool ok = true;
-    for (int j = b; j < n && ok; j += 2)
-      for (int x = 0; x < a.boxes; ++x, ++k) {
-        const int s = b * half_ring + k % half_ring;
-        if (!(ok = warp_wait(bar_empty(s), (k / half_ring & 1) ^ 1, abort_flag, a.status))) break;
+    for (int j = 0; j < n && ok; ++j)
+      for (int x = 0; x < a.boxes; ++x) {
+        if (!(ok = warp_wait(bar_empty(s), ph ^ 1, abort_flag, a.status))) break;
         if (elect_one()) {
           mbar_expect_tx(bar_full(s), kBoxBytes);
           tma_load_panels(sbase + a.off_ring + s * kBoxBytes, &tmD, tile_row(j), a.p.dx_panel + x,
                           bar_full(s));
         }
         __syncwarp();
+        ++issued;
+        if (++s == a.ring) { s = 0; ph ^= 1; }
       }
-    if (lane == 0) misc[2 + b] = static_cast<uint32_t>(k);
-  } else if (warp == 1 || warp == 3) {
-    const uint32_t idesc = idesc_bf16_f32(kTM, a.n_tile) | kBMnMajor;
+    if (lane == 0) misc[2] = static_cast<uint32_t>(issued);
+  } else if (warp == 1) {
+    const uint32_t idesc = idesc_bf16_f32(kTM, cols) | kBMnMajor;
     const int steps = a.p.ep / 16;                     // K steps of a term
     const uint64_t a0 = sdesc_k_sw128(sbase + a.off_ring), w0 = sdesc_mn_sw128(sbase, wblock);
-    const int b = warp >> 1;
-    const uint32_t acc = tmem + b * a.n_tile;
-    int k = 0;
+    int s = 0, ph = 0, consumed = 0;
     bool ok = true;
-    for (int j = b; j < n && ok; j += 2) {
+    for (int j = 0; j < n && ok; ++j) {
+      const int b = j & 1;
       if (!(ok = warp_wait(bar_free(b), ((j >> 1) & 1) ^ 1, abort_flag, a.status))) break;
       tc_fence_after();
+      const uint32_t acc = tmem + b * a.n_tile;
       int step = 0;                                    // ds's hi steps, then its mid steps
       for (int x = 0; x < a.boxes; ++x) {
-        const int s = b * half_ring + k % half_ring;
-        if (!(ok = warp_wait(bar_full(s), k / half_ring & 1, abort_flag, a.status))) break;
-        ++k;
+        if (!(ok = warp_wait(bar_full(s), ph, abort_flag, a.status))) break;
+        ++consumed;
         tc_fence_after();
         const uint64_t ad = advance(a0, static_cast<uint32_t>(s * kBoxBytes));
         if (elect_one()) {
@@ -818,36 +833,35 @@ __global__ void __launch_bounds__(kDxThreads, 1)
         }
         __syncwarp();
         step += 4;
+        if (++s == a.ring) { s = 0; ph ^= 1; }
       }
     }
-    if (lane == 0) misc[4 + b] = static_cast<uint32_t>(k);
+    if (lane == 0) misc[3] = static_cast<uint32_t>(consumed);
   } else if (warp == 2) {
-    auto hand_out = [&](int j) {                       // the staging buffer of tile j
-      const int s = j % a.staging;
+    const int total = n * units;
+    auto hand_out = [&](int q) {                       // the staging buffer of unit q
+      const int s = q % a.staging;
       if (!a.has_in) {
         mbar_arrive(bar_in(s));
         return;
       }
-      mbar_expect_tx(bar_in(s), static_cast<uint32_t>(staging_bytes));
-      for (int k = 0; k < blocks_n; ++k)
-        tma_load_2d(sbase + a.off_staging + s * staging_bytes + k * (kTM * 128), &tmIn, i0 + k * 64,
-                    tile_row(j), bar_in(s));
+      mbar_expect_tx(bar_in(s), kUnitBytes);
+      tma_load_2d(sbase + a.off_staging + s * kUnitBytes, &tmIn, i0 + q % units * 64,
+                  tile_row(q / units), bar_in(s));
     };
-    int out = n < a.staging ? n : a.staging;           // tiles whose buffer was handed out
+    int out = total < a.staging ? total : a.staging;   // units whose buffer was handed out
     if (elect_one())
-      for (int j = 0; j < out; ++j) hand_out(j);
+      for (int q = 0; q < out; ++q) hand_out(q);
     __syncwarp();
-    for (int j = 0; j < n; ++j) {
-      const int s = j % a.staging;
-      if (!warp_wait(bar_out(s), (j / a.staging) & 1, abort_flag, a.status)) break;
-      const bool more = j > 0 && out < n;
+    for (int q = 0; q < total; ++q) {
+      const int s = q % a.staging;
+      if (!warp_wait(bar_out(s), q / a.staging & 1, abort_flag, a.status)) break;
+      const bool more = q > 0 && out < total;
       if (elect_one()) {
-        for (int k = 0; k < blocks_n; ++k)
-          if (i0 + k * 64 < a.d)
-            tma_store_2d(&tmOut, sbase + a.off_staging + s * staging_bytes + k * (kTM * 128),
-                         i0 + k * 64, tile_row(j));
+        tma_store_2d(&tmOut, sbase + a.off_staging + s * kUnitBytes, i0 + q % units * 64,
+                     tile_row(q / units));
         bulk_commit();
-        bulk_wait_read<1>();                           // tile j - 1 has left its buffer
+        bulk_wait_read<1>();                           // unit q - 1 has left its buffer
         if (more) hand_out(out);
       }
       __syncwarp();
@@ -855,70 +869,70 @@ __global__ void __launch_bounds__(kDxThreads, 1)
     }
     if (elect_one()) bulk_wait_read<0>();              // the lane that issued the stores
     __syncwarp();
-    if (lane == 0) misc[6] = static_cast<uint32_t>(out);
-  } else if (warp < 4 + kOutWarps) {
+    if (lane == 0) misc[4] = static_cast<uint32_t>(out);
+  } else if (warp >= 4 && warp < 4 + kOutWarps) {
     const int quad = warp & 3, half = (warp - 4) >> 2, r = quad * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const int c0 = half * (a.n_tile / 2), c1 = c0 + a.n_tile / 2;
-    for (int j = 0; j < n; ++j) {
-      const int b = j & 1, s = j % a.staging;
-      bool ok = mbar_wait(bar_acc(b), (j >> 1) & 1, abort_flag, a.status);
-      ok = ok && mbar_wait(bar_in(s), (j / a.staging) & 1, abort_flag, a.status);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+    // this group's units, counted over all tiles: half, half + 2, ...
+    int waited = -1;
+    for (int q = half; q < n * units; q += 2) {
+      const int j = q / units, u = q % units, b = j & 1, s = q % a.staging;
+      for (; waited < j; ++waited)
+        if ((units > 1 || ((waited + 1) & 1) == half) &&
+            !warp_wait(bar_acc((waited + 1) & 1), (waited + 1) >> 1 & 1, abort_flag, a.status))
+          break;
+      if (waited < j) break;
+      if (!warp_wait(bar_in(s), q / a.staging & 1, abort_flag, a.status)) break;
       tc_fence_after();
-      uint8_t* row = smem + a.off_staging + s * staging_bytes + r * 128;
-#pragma unroll 2
-      for (int c = c0; c < c1; c += 16) {
+      uint8_t* row = smem + a.off_staging + s * kUnitBytes + r * 128;
+      const uint32_t acc = tmem + b * a.n_tile + lanes + u * 64;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
         uint32_t v[16];
-        tmem_ld16_sync(tmem + b * a.n_tile + lanes + c, v);
-        uint8_t* blk = row + (c >> 6) * (kTM * 128);
+        tmem_ld16_sync(acc + 16 * c, v);
+        if (c == 3) {
+          tc_fence_before();
+          __syncwarp();
+          if (u + 2 >= units && lane == 0) mbar_arrive(bar_free(b));
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint4* o = reinterpret_cast<uint4*>(blk + (((((c & 63) >> 3) + h) ^ (r & 7)) << 4));
-          float f[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v[8 * h + k]);
+          uint4* o = reinterpret_cast<uint4*>(row + (((2 * c + h) ^ (r & 7)) << 4));
+          uint32_t w[4] = {0, 0, 0, 0};
           if (a.has_in) {
-            const uint4 w4 = *o;
-            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              f[2 * k] += __uint_as_float(w[k] << 16);
-              f[2 * k + 1] += __uint_as_float(w[k] & 0xFFFF0000u);
-            }
+            const uint4 x = *o;
+            w[0] = x.x;
+            w[1] = x.y;
+            w[2] = x.z;
+            w[3] = x.w;
           }
-          uint32_t p[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const __nv_bfloat162 z = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
-            p[k] = *reinterpret_cast<const uint32_t*>(&z);
+            const __nv_bfloat162 z = __floats2bfloat162_rn(
+                __uint_as_float(v[8 * h + 2 * k]) + __uint_as_float(w[k] << 16),
+                __uint_as_float(v[8 * h + 2 * k + 1]) + __uint_as_float(w[k] & 0xFFFF0000u));
+            w[k] = *reinterpret_cast<const uint32_t*>(&z);
           }
-          *o = make_uint4(p[0], p[1], p[2], p[3]);
+          *o = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      tc_fence_before();
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar_free(b));
-        mbar_arrive(bar_out(s));
-      }
+      if (lane == 0) mbar_arrive(bar_out(s));
     }
+  } else if (warp >= 4 && a.sums.blocks) {
+    router_sums(a.sums, blockIdx.x, static_cast<int>(threadIdx.x) - 128 - 32 * kOutWarps,
+                32 * kSumsWarps);
   }
   tc_fence_before();
   __syncthreads();
   if (*abort_flag && threadIdx.x == 0) {
     // a wait gave up: loads in flight and issued UMMAs finish first (bounded)
-    const int G = a.staging;
-    for (int b = 0; b < 2; ++b) {
-      const int issued = static_cast<int>(misc[2 + b]), done = static_cast<int>(misc[4 + b]);
-      for (int k = issued > half_ring ? issued - half_ring : 0; k < issued; ++k)
-        drain_wait(bar_full(b * half_ring + k % half_ring), k / half_ring & 1);
-      for (int k = done > half_ring ? done - half_ring : 0; k < done; ++k)
-        drain_wait(bar_empty(b * half_ring + k % half_ring), k / half_ring & 1);
-    }
-    const int out = static_cast<int>(misc[6]);
-    for (int j = out > G ? out - G : 0; j < out; ++j) drain_wait(bar_in(j % G), j / G & 1);
+    const int R = a.ring, issued = static_cast<int>(misc[2]), done = static_cast<int>(misc[3]);
+    for (int k = issued > R ? issued - R : 0; k < issued; ++k) drain_wait(bar_full(k % R), k / R & 1);
+    for (int k = done > R ? done - R : 0; k < done; ++k) drain_wait(bar_empty(k % R), k / R & 1);
+    const int G = a.staging, out = static_cast<int>(misc[4]);
+    for (int q = out > G ? out - G : 0; q < out; ++q) drain_wait(bar_in(q % G), q / G & 1);
   }
   __syncthreads();
   if (warp == 3) {
@@ -935,6 +949,7 @@ int tmem_columns(int need) {
 
 struct Scratch {
   uint16_t* terms;
+  uint16_t* words;
   float* db_part;
   float* part;
   size_t bytes;
@@ -950,9 +965,11 @@ Scratch scratch_of(void* base, const Plan& p, int E, int T, int d) {
     return o;
   };
   const size_t terms = take(static_cast<size_t>(T) * p.all * 128);
+  const size_t words = take(static_cast<size_t>(padded_tokens(T)) * p.tiles_d * 8);
   const size_t db = take(static_cast<size_t>(p.term_blocks) * E * 4);
   const size_t part = take(static_cast<size_t>(p.splits) * E * d * 4);
   s.terms = reinterpret_cast<uint16_t*>(b + terms);
+  s.words = reinterpret_cast<uint16_t*>(b + words);
   s.db_part = reinterpret_cast<float*>(b + db);
   s.part = reinterpret_cast<float*>(b + part);
   s.bytes = off;
@@ -985,8 +1002,8 @@ cudaError_t launch_router_backward_tc(const RouterGradProblem& g, cudaStream_t s
   int lanes = 8;
   while (2 * lanes < p.ep) lanes *= 2;
   cudaError_t e = launch_kernel(router_terms_kernel, dim3(p.term_blocks), dim3(256), 0, st, g.dlogits,
-                                q8 ? g.rstd : nullptr, g.mask, g.E, g.T, p, lanes, sc.terms, sc.db_part,
-                                g.status);
+                                q8 ? g.rstd : nullptr, g.scales, g.mask, g.E, g.T, g.d, p, lanes, sc.terms,
+                                q8 ? sc.words : nullptr, sc.db_part, g.status);
   if (e != cudaSuccess) return e;
   pdl_launches() = true;
   auto encode_terms = [&](CUtensorMap* m, const cuuint32_t* box) {
@@ -997,17 +1014,17 @@ cudaError_t launch_router_backward_tc(const RouterGradProblem& g, cudaStream_t s
   if (g.dW) {
     DwArgs a;
     a.mask = g.mask;
-    a.q = g.q;
-    a.scales = g.scales;
+    a.words = sc.words;
     a.E = g.E;
     a.T = g.T;
     a.d = g.d;
     a.p = p;
-    a.stage_bytes = p.bt * 128 * (2 + p.panels);
+    a.stage_bytes = p.bt * 128 * (2 + p.panels) + (q8 ? (p.bt * 136 + 1023) / 1024 * 1024 : 0);
     a.stages = (kSmemLimit - kFixed) / a.stage_bytes;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
-    // an even number: a stage's buffer always belongs to the same issuer, which has
-    // waited for each of its phases (a parity tells only neighbouring ones apart)
+    // an even number: a buffer's phases all belong to one issuer and one group of
+    // converters, which have waited for each of them (a parity tells only
+    // neighbouring phases apart)
     a.stages &= ~1;
     a.tmem_cols = tmem_columns(2 * p.accs * p.egp);
     a.part = sc.part;
@@ -1017,22 +1034,29 @@ cudaError_t launch_router_backward_tc(const RouterGradProblem& g, cudaStream_t s
       const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.bt), static_cast<cuuint32_t>(p.panels)};
       if (!encode_terms(&tmD, box)) return cudaErrorInvalidValue;
     }
-    if (!q8) {
+    if (q8) {
+      const cuuint64_t dims[2] = {static_cast<cuuint64_t>(g.d), static_cast<cuuint64_t>(g.T)};
+      const cuuint64_t strides[1] = {static_cast<cuuint64_t>(g.d)};
+      const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(p.bt)};
+      if (!mx_make_bytes_map(&tmX, g.q, 2, dims, strides, box)) return cudaErrorInvalidValue;
+    } else {
       const cuuint64_t dims[2] = {static_cast<cuuint64_t>(g.d), static_cast<cuuint64_t>(g.T)};
       const cuuint64_t strides[1] = {static_cast<cuuint64_t>(g.d) * 2};
       const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(p.bt)};
       if (!mx_encode_bf16_map(&tmX, g.x, 2, dims, strides, box)) return cudaErrorInvalidValue;
     }
-    static bool done8[64] = {false}, done16[64] = {false};
+    static bool done[4][64] = {{false}};
     const dim3 grid(p.tiles_d * p.groups * p.splits);
+    const dim3 block(128 + 32 * (kSumWarps + (q8 ? kConvWarps : 0)));
     const size_t smem = static_cast<size_t>(a.stages) * a.stage_bytes + kFixed + 1024;
-    if (q8) {
-      if ((e = allow_smem(router_dw_kernel<true>, done8)) != cudaSuccess) return e;
-      e = launch_kernel(router_dw_kernel<true>, grid, dim3(128 + 32 * (kSumWarps + kConvWarps)), smem, st, tmX, tmD, a);
-    } else {
-      if ((e = allow_smem(router_dw_kernel<false>, done16)) != cudaSuccess) return e;
-      e = launch_kernel(router_dw_kernel<false>, grid, dim3(128 + 32 * kSumWarps), smem, st, tmX, tmD, a);
-    }
+    auto go = [&](auto kernel, bool (&set)[64]) {
+      const cudaError_t err = allow_smem(kernel, set);
+      return err != cudaSuccess ? err : launch_kernel(kernel, grid, block, smem, st, tmX, tmD, a);
+    };
+    if (q8)
+      e = p.bt == 64 ? go(router_dw_kernel<true, 64>, done[0]) : go(router_dw_kernel<true, 32>, done[1]);
+    else
+      e = p.bt == 64 ? go(router_dw_kernel<false, 64>, done[2]) : go(router_dw_kernel<false, 32>, done[3]);
     if (e != cudaSuccess) return e;
   }
   SumArgs sums;
@@ -1053,22 +1077,36 @@ cudaError_t launch_router_backward_tc(const RouterGradProblem& g, cudaStream_t s
     a.T = g.T;
     a.d = g.d;
     a.p = p;
-    a.n_tile = p.ep <= 128 ? 128 : 64;
-    a.tiles_n = (g.d + a.n_tile - 1) / a.n_tile;
+    // the widest tile whose part of W leaves room for four boxes and four units
+    a.n_tile = p.ep <= 96 ? 256 : p.ep <= 128 ? 192 : p.ep <= 192 ? 128 : 64;
+    a.full = g.d / a.n_tile;
+    const int part = (g.d - a.full * a.n_tile + 63) / 64, per = a.n_tile / 64;
     const int ttiles = (g.T + kTM - 1) / kTM;
-    a.splits = kPlanSms / a.tiles_n;
+    // CTAs in proportion to the columns, one per SM where d allows
+    a.splits = a.full ? kPlanSms * per / (a.full * per + part) : 0;
     if (a.splits > ttiles) a.splits = ttiles;
-    if (a.splits < 1) a.splits = 1;
+    if (a.full && a.splits < 1) a.splits = 1;
+    a.last_splits = 0;
+    if (part) {
+      a.last_splits = a.full ? (a.splits * part + per - 1) / per : kPlanSms;
+      const int left = kPlanSms - a.full * a.splits;
+      if (a.last_splits > left) a.last_splits = left;
+      if (a.last_splits > ttiles) a.last_splits = ttiles;
+      if (a.last_splits < 1) a.last_splits = 1;
+    }
     a.boxes = (2 * p.ep + 63) / 64;
-    const int wbytes = p.ep * 256 * (a.n_tile / 64), sbytes = a.n_tile / 64 * kTM * 128;
+    const int wbytes = p.ep * 256 * per;
     const int room = kSmemLimit - kFixed - wbytes;
-    a.staging = kMaxStaging;
-    while (a.staging > 2 && room - a.staging * sbytes < 6 * kBoxBytes) --a.staging;
-    a.ring = (room - a.staging * sbytes) / kBoxBytes;
-    a.ring = a.ring > kMaxRing ? kMaxRing : a.ring & ~1;
+    a.ring = room / 2 / kBoxBytes;
+    if (a.ring > 2 * a.boxes) a.ring = 2 * a.boxes;
+    a.ring = a.ring < 4 ? 4 : a.ring > kMaxRing ? kMaxRing : a.ring;
+    // an even number of units, so that a buffer's phases belong to one group of
+    // warps, which has waited for each (a parity tells only neighbouring ones apart)
+    a.staging = (room - a.ring * kBoxBytes) / kUnitBytes & ~1;
+    if (a.staging > kMaxStaging) a.staging = kMaxStaging;
     a.off_ring = wbytes;
     a.off_staging = a.off_ring + a.ring * kBoxBytes;
-    a.off_fixed = a.off_staging + a.staging * sbytes;
+    a.off_fixed = a.off_staging + a.staging * kUnitBytes;
     a.tmem_cols = tmem_columns(2 * a.n_tile);
     a.has_in = g.dx_in != nullptr;
     a.status = g.status;
@@ -1076,24 +1114,18 @@ cudaError_t launch_router_backward_tc(const RouterGradProblem& g, cudaStream_t s
     {
       const cuuint32_t box[3] = {64, kTM, 1};
       if (!encode_terms(&tmD, box)) return cudaErrorInvalidValue;
+      const cuuint64_t dims[2] = {static_cast<cuuint64_t>(g.d), static_cast<cuuint64_t>(g.T)};
+      const cuuint64_t strides[1] = {static_cast<cuuint64_t>(g.d) * 2};
+      if (!mx_encode_bf16_map(&tmOut, g.dx, 2, dims, strides, box)) return cudaErrorInvalidValue;
+      if (a.has_in && !mx_encode_bf16_map(&tmIn, g.dx_in, 2, dims, strides, box))
+        return cudaErrorInvalidValue;
     }
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(g.d), static_cast<cuuint64_t>(g.T)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(g.d) * 2};
-    const cuuint32_t box[2] = {64, kTM};
-    if (!mx_encode_bf16_map(&tmOut, g.dx, 2, dims, strides, box)) return cudaErrorInvalidValue;
-    if (a.has_in && !mx_encode_bf16_map(&tmIn, g.dx_in, 2, dims, strides, box)) return cudaErrorInvalidValue;
     static bool done[64] = {false};
     if ((e = allow_smem(router_dx_kernel, done)) != cudaSuccess) return e;
-    a.main_blocks = a.tiles_n * a.splits;
+    const int blocks = a.full * a.splits + a.last_splits;
     a.sums = sums;
-    a.sums.blocks = 0;
-    if (g.dW || g.db) {
-      const size_t items = g.dW ? static_cast<size_t>(g.E) * g.d / 4 : static_cast<size_t>(g.E) * 32;
-      const size_t most = a.main_blocks < kPlanSms / 2 ? kPlanSms - a.main_blocks : kPlanSms / 2;
-      const size_t want = (items + 2 * kDxThreads - 1) / (2 * kDxThreads);
-      a.sums.blocks = static_cast<int>(want < most ? want : most);
-    }
-    return launch_kernel(router_dx_kernel, dim3(a.main_blocks + a.sums.blocks), dim3(kDxThreads),
+    a.sums.blocks = g.dW || g.db ? blocks : 0;
+    return launch_kernel(router_dx_kernel, dim3(blocks), dim3(kDxThreads),
                       static_cast<size_t>(a.off_fixed) + kFixed + 1024, st, tmD, tmIn, tmOut, a);
   }
   if (!g.dW && !g.db) return cudaSuccess;
