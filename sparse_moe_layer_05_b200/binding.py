@@ -208,38 +208,52 @@ def _require_cuda(*ts) -> None:
             raise ValueError("expected contiguous tensors")
 
 
-_F32, _F16, _I32, _U8, _E4M3, _E8M0 = "f32", "bf16", "i32", "u8", "e4m3", "e8m0"
+# element types of the training calls' tensors: names, resolved to torch dtypes
+# on first use (torch is imported where it is needed only)
+_F32, _F16, _I32, _U8, _E4M3, _E8M0 = range(6)
+_KINDS = ("f32", "bf16", "i32", "u8", "e4m3", "e8m0")
 _DTYPES = None
+_torch_c = None
 
 
-def _args(**tensors) -> list:
-    """Pointers of the tensors of a training call, checked: CUDA, one device
-    (the current one), contiguous, and of the type and number of elements that
-    name=(tensor, type, elements) asks for; a None tensor gives a null pointer.
-    Without these checks a wrong size would be read past its end."""
-    import torch
-    global _DTYPES
+def _device() -> int:
+    """Index of the current CUDA device."""
+    global _DTYPES, _torch_c
     if _DTYPES is None:
-        _DTYPES = {_F32: (torch.float32,), _F16: (torch.bfloat16, torch.uint16),
-                   _I32: (torch.int32,), _U8: (torch.uint8, torch.bool),
-                   _E4M3: (torch.uint8, torch.float8_e4m3fn),
-                   _E8M0: (torch.uint8, torch.float8_e8m0fnu)}
-    cur = torch.cuda.current_device()
+        import torch
+        torch.cuda.init()
+        _torch_c = torch._C
+        _DTYPES = ((torch.float32,), (torch.bfloat16, torch.uint16), (torch.int32,),
+                   (torch.uint8, torch.bool), (torch.uint8, torch.float8_e4m3fn),
+                   (torch.uint8, torch.float8_e8m0fnu))
+    return _torch_c._cuda_getDevice()
+
+
+def _args(cur: int, specs) -> list:
+    """Pointers of the tensors of a training call, checked: on device ``cur`` (the
+    current one), contiguous, and of the type and number of elements that each
+    (name, tensor, type, elements) asks for; a None tensor gives a null pointer.
+    Without these checks a wrong size would be read past its end."""
     ptrs = []
-    for name, (t, kind, n) in tensors.items():
+    for name, t, kind, n in specs:
         if t is None:
             ptrs.append(None)
-            continue
-        if not t.is_cuda or t.get_device() != cur:
+        elif (t.get_device() == cur and t.dtype in _DTYPES[kind] and t.numel() == n
+              and t.is_contiguous()):
+            ptrs.append(t.data_ptr())
+        elif t.get_device() != cur:
             raise ValueError(f"{name}: expected a tensor on the current CUDA device")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: expected a contiguous tensor")
-        if t.dtype not in _DTYPES[kind]:
-            raise ValueError(f"{name}: expected {kind} elements, got {t.dtype}")
-        if t.numel() != n:
+        elif t.dtype not in _DTYPES[kind]:
+            raise ValueError(f"{name}: expected {_KINDS[kind]} elements, got {t.dtype}")
+        elif t.numel() != n:
             raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
-        ptrs.append(t.data_ptr())
+        else:
+            raise ValueError(f"{name}: expected a contiguous tensor")
     return ptrs
+
+
+def _raw_stream(stream, cur: int) -> int:
+    return int(stream.cuda_stream) if stream is not None else _torch_c._cuda_getCurrentRawStream(cur)
 
 
 # ---------------------------------------------------------------- sizes ----
@@ -441,14 +455,19 @@ def moe_balance_loss(logits, topk_idx, E: int, k: int, T: int, balance_coef: flo
     """Load-balance and z loss of logits [T, E] f32 with the per-expert counts:
     stats f32 [4] (loss, balance, z, live tokens), counts i32 [E], mean_probs
     f32 [E], lse f32 [T]. token_mask u8 or bool [T]: 0 leaves a token out."""
-    lo, ix, mk, sa, co, mp, ls, ws = _args(
-        logits=(logits, _F32, T * E), topk_idx=(topk_idx, _I32, T * k),
-        token_mask=(token_mask, _U8, T), stats=(stats, _F32, 4), counts=(counts, _I32, E),
-        mean_probs=(mean_probs, _F32, E), lse=(lse, _F32, T),
-        workspace=(workspace, _U8, workspace.numel()))
+    cur = _device()
+    lo, ix, mk, sa, co, mp, ls, ws = _args(cur, (
+        ("logits", logits, _F32, T * E),
+        ("topk_idx", topk_idx, _I32, T * k),
+        ("token_mask", token_mask, _U8, T),
+        ("stats", stats, _F32, 4),
+        ("counts", counts, _I32, E),
+        ("mean_probs", mean_probs, _F32, E),
+        ("lse", lse, _F32, T),
+        ("workspace", workspace, _U8, workspace.numel())))
     _check("moe_balance_loss", load().moe_balance_loss(
         lo, ix, mk, E, k, T, balance_coef, z_coef, sa, co, mp, ls, ws, workspace.numel(),
-        _stream(stream)))
+        _raw_stream(stream, cur)))
 
 
 def moe_balance_loss_backward(logits, lse, counts, stats, E: int, k: int, T: int,
@@ -456,25 +475,34 @@ def moe_balance_loss_backward(logits, lse, counts, stats, E: int, k: int, T: int
                               token_mask=None, accumulate: bool = False, stream=None) -> None:
     """dlogits [T, E] f32 (+)= gradient of moe_balance_loss; dloss f32 [1] on the
     device (None: 1)."""
-    lo, ls, co, sa, mk, dv, dl = _args(
-        logits=(logits, _F32, T * E), lse=(lse, _F32, T), counts=(counts, _I32, E),
-        stats=(stats, _F32, 4), token_mask=(token_mask, _U8, T), dloss=(dloss, _F32, 1),
-        dlogits=(dlogits, _F32, T * E))
+    cur = _device()
+    lo, ls, co, sa, mk, dv, dl = _args(cur, (
+        ("logits", logits, _F32, T * E),
+        ("lse", lse, _F32, T),
+        ("counts", counts, _I32, E),
+        ("stats", stats, _F32, 4),
+        ("token_mask", token_mask, _U8, T),
+        ("dloss", dloss, _F32, 1),
+        ("dlogits", dlogits, _F32, T * E)))
     _check("moe_balance_loss_backward", load().moe_balance_loss_backward(
         lo, ls, co, sa, mk, E, k, T, balance_coef, z_coef, dv, int(accumulate), dl,
-        _stream(stream)))
+        _raw_stream(stream, cur)))
 
 
 def moe_gate_backward(dout, yw, topk_idx, topk_w, E: int, k: int, T: int, d: int, dlogits,
                       token_mask=None, accumulate: bool = False, stream=None) -> None:
     """dlogits [T, E] f32 (+)= gradient through the selected-set softmax, from
     dout bf16 [T, d] and the weighted expert rows yw f32 [T*k, d]."""
-    do, yp, ix, wp, mk, dl = _args(
-        dout=(dout, _F16, T * d), yw=(yw, _F32, T * k * d), topk_idx=(topk_idx, _I32, T * k),
-        topk_w=(topk_w, _F32, T * k), token_mask=(token_mask, _U8, T),
-        dlogits=(dlogits, _F32, T * E))
+    cur = _device()
+    do, yp, ix, wp, mk, dl = _args(cur, (
+        ("dout", dout, _F16, T * d),
+        ("yw", yw, _F32, T * k * d),
+        ("topk_idx", topk_idx, _I32, T * k),
+        ("topk_w", topk_w, _F32, T * k),
+        ("token_mask", token_mask, _U8, T),
+        ("dlogits", dlogits, _F32, T * E)))
     _check("moe_gate_backward", load().moe_gate_backward(
-        do, yp, ix, wp, mk, E, k, T, d, int(accumulate), dl, _stream(stream)))
+        do, yp, ix, wp, mk, E, k, T, d, int(accumulate), dl, _raw_stream(stream, cur)))
 
 
 def moe_router_backward(dlogits, W_r, E: int, T: int, d: int, dW, db, dx, workspace, x=None,
@@ -483,26 +511,40 @@ def moe_router_backward(dlogits, W_r, E: int, T: int, d: int, dW, db, dx, worksp
     """dW f32 [E, d], db f32 [E], dx bf16 [T, d] (each may be None) from dlogits
     f32 [T, E]; the input rows as x bf16 [T, d], or as the checkpoint q, scales,
     rstd with the norm's gain g."""
-    dl, wr, xp, qp, sp, rp, gp, mk, di, dw, bp, dp, ws = _args(
-        dlogits=(dlogits, _F32, T * E), W_r=(W_r, _F32, E * d), x=(x, _F16, T * d),
-        q=(q, _E4M3, T * d), scales=(scales, _E8M0, T * (d // 32)), rstd=(rstd, _F32, T),
-        g=(g, _F32, d), token_mask=(token_mask, _U8, T), dx_in=(dx_in, _F16, T * d),
-        dW=(dW, _F32, E * d), db=(db, _F32, E), dx=(dx, _F16, T * d),
-        workspace=(workspace, _U8, workspace.numel()))
+    cur = _device()
+    dl, wr, xp, qp, sp, rp, gp, mk, di, dw, bp, dp, ws = _args(cur, (
+        ("dlogits", dlogits, _F32, T * E),
+        ("W_r", W_r, _F32, E * d),
+        ("x", x, _F16, T * d),
+        ("q", q, _E4M3, T * d),
+        ("scales", scales, _E8M0, T * (d // 32)),
+        ("rstd", rstd, _F32, T),
+        ("g", g, _F32, d),
+        ("token_mask", token_mask, _U8, T),
+        ("dx_in", dx_in, _F16, T * d),
+        ("dW", dW, _F32, E * d),
+        ("db", db, _F32, E),
+        ("dx", dx, _F16, T * d),
+        ("workspace", workspace, _U8, workspace.numel())))
     _check("moe_router_backward", load().moe_router_backward(
         dl, wr, xp, qp, sp, rp, gp, mk, E, T, d, di, int(accumulate), dw, bp, dp, ws,
-        workspace.numel(), _stream(stream)))
+        workspace.numel(), _raw_stream(stream, cur)))
 
 
 def moe_rms_norm_checkpoint(h, g, eps: float, T: int, d: int, x, q, scales, rstd,
                             stream=None) -> None:
     """moe_rms_norm that also leaves h as an 8-bit checkpoint: q E4M3 [T, d],
     scales E8M0 [T, d/32], and rstd f32 [T]; x may be None."""
-    hp, gp, xp, qp, sp, rp = _args(
-        h=(h, _F16, T * d), g=(g, _F32, d), x=(x, _F16, T * d), q=(q, _E4M3, T * d),
-        scales=(scales, _E8M0, T * (d // 32)), rstd=(rstd, _F32, T))
+    cur = _device()
+    hp, gp, xp, qp, sp, rp = _args(cur, (
+        ("h", h, _F16, T * d),
+        ("g", g, _F32, d),
+        ("x", x, _F16, T * d),
+        ("q", q, _E4M3, T * d),
+        ("scales", scales, _E8M0, T * (d // 32)),
+        ("rstd", rstd, _F32, T)))
     _check("moe_rms_norm_checkpoint", load().moe_rms_norm_checkpoint(
-        hp, gp, eps, T, d, xp, qp, sp, rp, _stream(stream)))
+        hp, gp, eps, T, d, xp, qp, sp, rp, _raw_stream(stream, cur)))
 
 
 def moe_rms_norm_backward(dx, g, rstd, T: int, d: int, dh, dg, workspace, h=None, q=None,
@@ -510,14 +552,22 @@ def moe_rms_norm_backward(dx, g, rstd, T: int, d: int, dh, dg, workspace, h=None
                           stream=None) -> None:
     """dh bf16 [T, d] and dg f32 [d] of the norm, from its bf16 input rows h or
     their checkpoint q, scales."""
-    dp, hp, qp, sp, rp, gp, mk, di, oh, og, ws = _args(
-        dx=(dx, _F16, T * d), h=(h, _F16, T * d), q=(q, _E4M3, T * d),
-        scales=(scales, _E8M0, T * (d // 32)), rstd=(rstd, _F32, T), g=(g, _F32, d),
-        token_mask=(token_mask, _U8, T), dh_in=(dh_in, _F16, T * d), dh=(dh, _F16, T * d),
-        dg=(dg, _F32, d), workspace=(workspace, _U8, workspace.numel()))
+    cur = _device()
+    dp, hp, qp, sp, rp, gp, mk, di, oh, og, ws = _args(cur, (
+        ("dx", dx, _F16, T * d),
+        ("h", h, _F16, T * d),
+        ("q", q, _E4M3, T * d),
+        ("scales", scales, _E8M0, T * (d // 32)),
+        ("rstd", rstd, _F32, T),
+        ("g", g, _F32, d),
+        ("token_mask", token_mask, _U8, T),
+        ("dh_in", dh_in, _F16, T * d),
+        ("dh", dh, _F16, T * d),
+        ("dg", dg, _F32, d),
+        ("workspace", workspace, _U8, workspace.numel())))
     _check("moe_rms_norm_backward", load().moe_rms_norm_backward(
         dp, hp, qp, sp, rp, gp, mk, T, d, di, int(accumulate), oh, og, ws, workspace.numel(),
-        _stream(stream)))
+        _raw_stream(stream, cur)))
 
 
 def moe_forward_block_checkpoint(h, g, eps: float, W_r, b_r, Wgu_codes, Wgu_scales, Wd_codes,
@@ -527,8 +577,8 @@ def moe_forward_block_checkpoint(h, g, eps: float, W_r, b_r, Wgu_codes, Wgu_scal
     """moe_forward_block that also leaves the norm's 8-bit checkpoint."""
     _require_cuda(h, g, W_r, b_r, Wgu_codes, Wgu_scales, gu_bias, Wd_codes, Wd_scales, down_bias,
                   out, workspace)
-    qp, sp, rp = _args(q=(q, _E4M3, T * d), scales=(scales, _E8M0, T * (d // 32)),
-                       rstd=(rstd, _F32, T))
+    qp, sp, rp = _args(_device(), (("q", q, _E4M3, T * d), ("scales", scales, _E8M0, T * (d // 32)),
+                                   ("rstd", rstd, _F32, T)))
     _check("moe_forward_block_checkpoint", load().moe_forward_block_checkpoint(
         _ptr(h), _ptr(g), eps, _ptr(W_r), _ptr(b_r), _ptr(Wgu_codes), _ptr(Wgu_scales),
         _ptr(gu_bias), _ptr(Wd_codes), _ptr(Wd_scales), _ptr(down_bias), E, k, T, d, I,

@@ -22,64 +22,159 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// One warp per row; sum of squares, root and division are those of the norm
-// without a checkpoint, in the same order, so x is the same bit for bit.
-__global__ void __launch_bounds__(256) norm_ckpt_kernel(const uint16_t* __restrict__ h,
-                                                        const float* __restrict__ g, float eps,
-                                                        int T, int d, uint16_t* __restrict__ x,
-                                                        uint8_t* __restrict__ q,
-                                                        uint8_t* __restrict__ scales,
-                                                        float* __restrict__ rstd) {
+__device__ __forceinline__ void unpack2(uint32_t v, float* f) {
+  f[0] = __uint_as_float(v << 16);
+  f[1] = __uint_as_float(v & 0xFFFF0000u);
+}
+
+// Two fp32 operations in one instruction, each rounded as its own.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 bf16_pair(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+
+// a / b correctly rounded, y = 1 / b correctly rounded: q = a y is within an ulp
+// of the quotient, a - b q is exact, and q + y (a - b q) rounds to the quotient
+// (P. Markstein, IBM J. Res. Dev. 34, 1990), as long as nothing underflows or
+// overflows: the caller keeps |a| and b between 2^-60 and 2^60. Three
+// instructions; the division operator's dozen per element were a third of the
+// kernel's.
+__device__ __forceinline__ float2 quotient2(float2 a, float b, float y) {
+  const float2 q = mul2(a, both(y));
+  return fma2(fma2(both(-b), q, a), both(y), q);
+}
+
+__device__ __forceinline__ void async_copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void async_copies_done() {
+  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+}
+
+// One warp per row in turn, the row in shared memory. The sum of squares and the
+// root are those of the norm without a checkpoint, in the same order, so x is the
+// same bit for bit: lane l sums elements 4 l .. 4 l + 3 of each 128. Then each lane
+// converts eight elements at a time (four lanes share a group's scale) and, as
+// soon as it has read them, loads the next row's into their place.
+constexpr int kCkptWarps = 4;
+
+__global__ void __launch_bounds__(kCkptWarps * 32, 9) norm_ckpt_kernel(
+    const uint16_t* __restrict__ h, const float* __restrict__ g, float eps, int T, int d,
+    uint16_t* __restrict__ x, uint8_t* __restrict__ q, uint8_t* __restrict__ scales,
+    float* __restrict__ rstd) {
   pdl_wait_and_trigger();
+  extern __shared__ __align__(16) uint8_t rows[];
+  constexpr float kLo = 8.673617379884035e-19f, kHi = 1.152921504606847e18f;   // 2^-60, 2^60
   const int lane = threadIdx.x & 31;
-  const int nwarps = (gridDim.x * blockDim.x) >> 5;
-  for (int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; t < T; t += nwarps) {
-    const uint16_t* hr = h + (size_t)t * d;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kCkptWarps;
+  const uint8_t* const row = rows + static_cast<size_t>(threadIdx.x >> 5) * d * 2;
+  const uint32_t row_s = smem_u32(row);
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kCkptWarps + (threadIdx.x >> 5);
+  if (t < T)
+    for (int k = lane * 8; k < d; k += 256) async_copy16(row_s + k * 2, h + t * d + k);
+  for (; t < T; t += step) {
+    async_copies_done();
+    __syncwarp();
     float ss = 0.f;
+#pragma unroll 4
     for (int k = lane * 4; k < d; k += 128) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(hr + k));
-      const float a = __uint_as_float(v.x << 16), b = __uint_as_float(v.x & 0xFFFF0000u);
-      const float c = __uint_as_float(v.y << 16), e = __uint_as_float(v.y & 0xFFFF0000u);
-      ss = fmaf(a, a, ss);
-      ss = fmaf(b, b, ss);
-      ss = fmaf(c, c, ss);
-      ss = fmaf(e, e, ss);
+      const uint2 v = *reinterpret_cast<const uint2*>(row + k * 2);
+      float f[4];
+      unpack2(v.x, f);
+      unpack2(v.y, f + 2);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ss = fmaf(f[i], f[i], ss);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
     const float root = sqrtf(ss / (float)d + eps);
-    if (lane == 0) rstd[t] = 1.f / root;
-    for (int k0 = 0; k0 < d; k0 += 128) {
-      const int k = k0 + lane * 4;
-      const bool in = k < d;   // whole groups of 8 lanes: d is a multiple of 32
-      const uint2 v = in ? __ldg(reinterpret_cast<const uint2*>(hr + k)) : make_uint2(0, 0);
-      const float f0 = __uint_as_float(v.x << 16), f1 = __uint_as_float(v.x & 0xFFFF0000u);
-      const float f2 = __uint_as_float(v.y << 16), f3 = __uint_as_float(v.y & 0xFFFF0000u);
-      float amax = fmaxf(fmaxf(fabsf(f0), fabsf(f1)), fmaxf(fabsf(f2), fabsf(f3)));
+    const float y = 1.f / root;
+    if (lane == 0) rstd[t] = y;
+    const bool plain = root >= kLo && root <= kHi;
+    uint8_t* const qr = q + t * d;
+    uint8_t* const sr = scales + t * (d / 32);
+    uint16_t* const xr = x + t * d;
+    const uint16_t* const next = h + (t + step) * d;
+    const bool more = t + step < T;
+#pragma unroll 2
+    for (int k0 = 0; k0 < d; k0 += 256) {
+      const int k = k0 + lane * 8;
+      const bool in = k < d;   // whole groups of four lanes: d is a multiple of 32
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (in) {
+        v = *reinterpret_cast<const uint4*>(row + k * 2);
+        if (more) async_copy16(row_s + k * 2, next + k);
+      }
+      float f[8];
+      unpack2(v.x, f);
+      unpack2(v.y, f + 2);
+      unpack2(v.z, f + 4);
+      unpack2(v.w, f + 6);
+      float amax = fabsf(f[0]), amin = fabsf(f[0]);
 #pragma unroll
-      for (int off = 4; off > 0; off >>= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
+      for (int i = 1; i < 8; ++i) {
+        amax = fmaxf(amax, fabsf(f[i]));
+        amin = fminf(amin, fabsf(f[i]));
+      }
+      const bool fast = plain && amin >= kLo && amax <= kHi;
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
       if (!in) continue;
       const int ex = mx_scale_exp<ACT_E4M3>(amax);
       const float inv = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-      *reinterpret_cast<uint32_t*>(q + (size_t)t * d + k) =
-          f32x2_to_e4m3x2(f0 * inv, f1 * inv) | (f32x2_to_e4m3x2(f2 * inv, f3 * inv) << 16);
-      if ((lane & 7) == 0)
-        scales[(size_t)t * (d / 32) + k / 32] = static_cast<uint8_t>(ex + 127);
+      float2 z[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[i] = mul2(make_float2(f[2 * i], f[2 * i + 1]), both(inv));
+      *reinterpret_cast<uint2*>(qr + k) =
+          make_uint2(f32x2_to_e4m3x2(z[0].x, z[0].y) | (f32x2_to_e4m3x2(z[1].x, z[1].y) << 16),
+                     f32x2_to_e4m3x2(z[2].x, z[2].y) | (f32x2_to_e4m3x2(z[3].x, z[3].y) << 16));
+      if ((lane & 3) == 0) sr[k / 32] = static_cast<uint8_t>(ex + 127);
       if (x) {
-        const float4 gv = __ldg(reinterpret_cast<const float4*>(g + k));
-        *reinterpret_cast<uint2*>(x + (size_t)t * d + k) =
-            make_uint2(pack_bf16((f0 / root) * gv.x, (f1 / root) * gv.y),
-                       pack_bf16((f2 / root) * gv.z, (f3 / root) * gv.w));
+        const float4 g0 = __ldg(reinterpret_cast<const float4*>(g + k));
+        const float4 g1 = __ldg(reinterpret_cast<const float4*>(g + k) + 1);
+        const float2 gv[4] = {make_float2(g0.x, g0.y), make_float2(g0.z, g0.w),
+                              make_float2(g1.x, g1.y), make_float2(g1.z, g1.w)};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 a = make_float2(f[2 * i], f[2 * i + 1]);
+          const float2 n = mul2(fast ? quotient2(a, root, y) : make_float2(a.x / root, a.y / root), gv[i]);
+          o[i] = pack_bf16(n.x, n.y);
+        }
+        *reinterpret_cast<uint4*>(xr + k) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
 }
 
 // One block per row in turn, each thread eight columns per chunk: the gain's
-// gradient of those columns stays in registers over the block's rows.
+// gradient of those columns stays in registers over the block's rows. The next
+// row's loads run while this row's mean is formed.
+constexpr int kNormThreads = 512;
+
+struct NormRow {
+  uint4 dx, h;         // h: 8 bf16, or 8 codes in .x and .y
+  uint32_t scale;
+};
+
 template <bool Q8, int NC>
-__global__ void __launch_bounds__(1024) norm_backward_kernel(
+__global__ void __maxnreg__(NC == 1 ? 56 : 128) norm_backward_kernel(
     const uint16_t* dx, const uint16_t* __restrict__ h, const uint8_t* __restrict__ q,
     const uint8_t* __restrict__ scales, const float* __restrict__ rstd,
     const float* __restrict__ g, const uint8_t* __restrict__ mask, int T, int d,
@@ -88,117 +183,152 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(
   __shared__ float red[2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int vec = d / 8;
-  float dg[NC][8];
+  float2 dg[NC][4];
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dg[c][i] = 0.f;
-  int buf = 0;
-  for (int t = blockIdx.x; t < T; t += gridDim.x) {
-    const bool live = mask == nullptr || mask[t] != 0;
-    const float r = rstd[t];
-    float n[NC][8], u[NC][8];
-    float dot = 0.f;
-    if (live) {
+    for (int i = 0; i < 4; ++i) dg[c][i] = make_float2(0.f, 0.f);
+  NormRow next[NC];
+  uint4 in[NC];
+  float next_r = 0.f;
+  uint32_t next_live = 1;
+  // whether or not the token is live: no load waits for the mask's
+  auto load = [&](int t) {
+    if (t >= T) return;
+    next_r = __ldg(rstd + t);
+    if (mask) next_live = __ldg(mask + t);
+    const int64_t row = static_cast<int64_t>(t) * d;
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int v = threadIdx.x + c * blockDim.x;
-        if (v >= vec) continue;
-        const uint4 dv = reinterpret_cast<const uint4*>(dx + (size_t)t * d)[v];
-        const uint32_t dw[4] = {dv.x, dv.y, dv.z, dv.w};
-        float hv[8];
-        if (Q8) {
-          const uint2 qv = __ldg(reinterpret_cast<const uint2*>(q + (size_t)t * d) + v);
-          const float s = e8m0_to_f32(scales[(size_t)t * (d / 32) + v / 4]);
-          const uint32_t qw[2] = {qv.x, qv.y};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = e4m3x2_to_f32x2((qw[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-            hv[2 * i] = f.x * s;
-            hv[2 * i + 1] = f.y * s;
-          }
-        } else {
-          const uint4 hw4 = __ldg(reinterpret_cast<const uint4*>(h + (size_t)t * d) + v);
-          const uint32_t hw[4] = {hw4.x, hw4.y, hw4.z, hw4.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            hv[2 * i] = __uint_as_float(hw[i] << 16);
-            hv[2 * i + 1] = __uint_as_float(hw[i] & 0xFFFF0000u);
-          }
-        }
-        const float4 g0 = __ldg(reinterpret_cast<const float4*>(g) + 2 * v);
-        const float4 g1 = __ldg(reinterpret_cast<const float4*>(g) + 2 * v + 1);
-        const float gv[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float dxv = __uint_as_float(i & 1 ? dw[i >> 1] & 0xFFFF0000u : dw[i >> 1] << 16);
-          n[c][i] = hv[i] * r;
-          u[c][i] = dxv * gv[i];
-          dg[c][i] = fmaf(dxv, n[c][i], dg[c][i]);
-          dot = fmaf(n[c][i], u[c][i], dot);
-        }
+    for (int c = 0; c < NC; ++c) {
+      const int v = threadIdx.x + c * blockDim.x;
+      if (v >= vec) continue;
+      next[c].dx = *reinterpret_cast<const uint4*>(dx + row + v * 8);
+      if (Q8) {
+        const uint2 w = __ldcs(reinterpret_cast<const uint2*>(q + row + v * 8));
+        next[c].h.x = w.x;
+        next[c].h.y = w.y;
+        next[c].scale = __ldg(scales + (row >> 5) + (v >> 2));
+      } else {
+        next[c].h = __ldcs(reinterpret_cast<const uint4*>(h + row + v * 8));
       }
     }
+  };
+  auto load_in = [&](int t) {
+    if (t >= T || !dh_in) return;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int v = threadIdx.x + c * blockDim.x;
+      if (v < vec) in[c] = *reinterpret_cast<const uint4*>(dh_in + static_cast<int64_t>(t) * d + v * 8);
+    }
+  };
+  const float inv_d = 1.f / static_cast<float>(d);
+  int buf = 0;
+  int t = blockIdx.x;
+  load(t);
+  load_in(t);
+  for (; t < T; t += gridDim.x) {
+    const bool live = next_live != 0;
+    // a padded token's row: r = 0 and its values are not looked at
+    const float r = live ? next_r : 0.f;
+    float2 n[NC][4], u[NC][4];
+    float2 dots = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int v = threadIdx.x + c * blockDim.x;
+      if (v >= vec) continue;
+      if (!live) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n[c][i] = u[c][i] = make_float2(0.f, 0.f);
+        continue;
+      }
+      const uint32_t dw[4] = {next[c].dx.x, next[c].dx.y, next[c].dx.z, next[c].dx.w};
+      if (Q8) {
+        const float2 s = both(e8m0_to_f32(next[c].scale));
+        const uint32_t hw[2] = {next[c].h.x, next[c].h.y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          n[c][i] = mul2(mul2(e4m3x2_to_f32x2((hw[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), s), both(r));
+      } else {
+        const uint32_t hw[4] = {next[c].h.x, next[c].h.y, next[c].h.z, next[c].h.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n[c][i] = mul2(bf16_pair(hw[i]), both(r));
+      }
+      const float4 g0 = __ldg(reinterpret_cast<const float4*>(g) + 2 * v);
+      const float4 g1 = __ldg(reinterpret_cast<const float4*>(g) + 2 * v + 1);
+      const float2 gv[4] = {make_float2(g0.x, g0.y), make_float2(g0.z, g0.w), make_float2(g1.x, g1.y),
+                            make_float2(g1.z, g1.w)};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 x = bf16_pair(dw[i]);
+        dg[c][i] = fma2(x, n[c][i], dg[c][i]);
+        u[c][i] = mul2(x, gv[i]);
+        dots = fma2(n[c][i], u[c][i], dots);
+      }
+    }
+    float dot = dots.x + dots.y;
+    load(t + gridDim.x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, off);
     if (lane == 0) red[buf][warp] = dot;
     __syncthreads();
-    float m = 0.f;
-    for (int w = 0; w < warps; ++w) m += red[buf][w];
-    m /= (float)d;
+    float m = lane < warps ? red[buf][lane] : 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m += __shfl_xor_sync(0xFFFFFFFFu, m, off);
+    m *= -r * inv_d;
     buf ^= 1;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int v = threadIdx.x + c * blockDim.x;
       if (v >= vec) continue;
-      float o[8];
+      // dh_in + r u - (r mean) n
+      const uint32_t dw[4] = {in[c].x, in[c].y, in[c].z, in[c].w};
+      uint32_t o[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = live ? r * (u[c][i] - n[c][i] * m) : 0.f;
-      if (dh_in) {
-        const uint4 dv = reinterpret_cast<const uint4*>(dh_in + (size_t)t * d)[v];
-        const uint32_t dw[4] = {dv.x, dv.y, dv.z, dv.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          o[2 * i] += __uint_as_float(dw[i] << 16);
-          o[2 * i + 1] += __uint_as_float(dw[i] & 0xFFFF0000u);
-        }
+      for (int i = 0; i < 4; ++i) {
+        float2 z = fma2(both(m), n[c][i], mul2(both(r), u[c][i]));
+        if (dh_in) z = fma2(z, both(1.f), bf16_pair(dw[i]));
+        o[i] = pack_bf16(z.x, z.y);
       }
-      reinterpret_cast<uint4*>(dh + (size_t)t * d)[v] =
-          make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
-                     pack_bf16(o[6], o[7]));
+      *reinterpret_cast<uint4*>(dh + static_cast<int64_t>(t) * d + v * 8) =
+          make_uint4(o[0], o[1], o[2], o[3]);
     }
+    load_in(t + gridDim.x);
   }
-  float* pr = partial + (size_t)blockIdx.x * d;
+  float* pr = partial + static_cast<size_t>(blockIdx.x) * d;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int v = threadIdx.x + c * blockDim.x;
     if (v >= vec) continue;
-    reinterpret_cast<float4*>(pr)[2 * v] = make_float4(dg[c][0], dg[c][1], dg[c][2], dg[c][3]);
-    reinterpret_cast<float4*>(pr)[2 * v + 1] = make_float4(dg[c][4], dg[c][5], dg[c][6], dg[c][7]);
+    reinterpret_cast<float4*>(pr)[2 * v] =
+        make_float4(dg[c][0].x, dg[c][0].y, dg[c][1].x, dg[c][1].y);
+    reinterpret_cast<float4*>(pr)[2 * v + 1] =
+        make_float4(dg[c][2].x, dg[c][2].y, dg[c][3].x, dg[c][3].y);
   }
 }
 
-// dg[i] (+)= sum over the blocks' rows, in block order within each of eight
-// shares, the shares in order.
-__global__ void __launch_bounds__(256) norm_dg_kernel(const float* __restrict__ partial, int rows,
-                                                      int d, bool accumulate,
-                                                      float* __restrict__ dg) {
+// dg[i] (+)= sum over the blocks' rows, in block order within each of 32 shares,
+// the shares in order.
+__global__ void __launch_bounds__(1024) norm_dg_kernel(const float* __restrict__ partial, int rows,
+                                                       int d, bool accumulate,
+                                                       float* __restrict__ dg) {
   pdl_wait_and_trigger();
-  __shared__ float sh[8][32];
+  __shared__ float sh[32][33];
   const int lane = threadIdx.x & 31, share = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + lane;   // d is a multiple of 32
   float s = 0.f;
-  for (int r = share; r < rows; r += 8) s += __ldg(partial + (size_t)r * d + i);
+#pragma unroll 16
+  for (int r = share; r < rows; r += 32) s += __ldg(partial + static_cast<size_t>(r) * d + i);
   sh[share][lane] = s;
   __syncthreads();
-  if (share == 0) {
+  // warp w: column w of the block's 32
+  s = sh[lane][share];
 #pragma unroll
-    for (int w = 1; w < 8; ++w) s += sh[w][lane];
-    dg[i] = accumulate ? dg[i] + s : s;
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+  if (lane == 0) {
+    float* o = dg + blockIdx.x * 32 + share;
+    *o = accumulate ? *o + s : s;
   }
 }
-
-constexpr int kNormBwdBlocks = 148 * 4;
 
 struct NormBwdShape {
   int threads, chunks, blocks;
@@ -207,10 +337,14 @@ struct NormBwdShape {
 NormBwdShape norm_bwd_shape(int T, int d) {
   NormBwdShape s;
   const int vec = d / 8;                         // at most 2048
-  s.chunks = vec > 1024 ? 2 : 1;
-  s.threads = (vec / s.chunks + 31) / 32 * 32;
-  while (s.threads * s.chunks < vec) s.threads += 32;
-  s.blocks = T < kNormBwdBlocks ? (T > 0 ? T : 1) : kNormBwdBlocks;
+  s.chunks = vec <= kNormThreads ? 1 : vec <= 2 * kNormThreads ? 2 : 4;
+  s.threads = ((vec + s.chunks - 1) / s.chunks + 31) / 32 * 32;
+  // blocks that fill an SM's threads about half, at most three where rows are long
+  // (each leaves a row of partial sums: at d = 2880 three leave 5 MB, beside 165 MB
+  // of rows at T = 8192) and sixteen where they are short
+  int per = 1152 / s.threads;
+  per = per < 1 ? 1 : per > 16 ? 16 : per;
+  s.blocks = T < 148 * per ? (T > 0 ? T : 1) : 148 * per;
   return s;
 }
 
@@ -219,10 +353,24 @@ NormBwdShape norm_bwd_shape(int T, int d) {
 cudaError_t launch_rms_norm_checkpoint(const uint16_t* h, const float* g, float eps, int T, int d,
                                        uint16_t* x, uint8_t* q, uint8_t* scales, float* rstd,
                                        cudaStream_t st) {
-  const int64_t b = (static_cast<int64_t>(T) + 7) / 8;
-  const int grid = static_cast<int>(b < 148 * 8 ? b : 148 * 8);
-  return launch_kernel(norm_ckpt_kernel, dim3(grid), dim3(256), 0, st, h, g, eps, T, d, x, q,
-                       scales, rstd);
+  // as many blocks as an SM holds (T = 8192, d = 2880: 47 us with 12 warps per SM, 37
+  // with 20, 31 with 32), at most 36 warps of them
+  const size_t smem = static_cast<size_t>(kCkptWarps) * d * 2;
+  static bool set[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(norm_ckpt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kCkptWarps * 16384 * 2);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) set[dev] = true;
+  }
+  int per = static_cast<int>(225 * 1024 / (smem + 1024));
+  per = per < 1 ? 1 : per > 9 ? 9 : per;
+  const int64_t b = (static_cast<int64_t>(T) + kCkptWarps - 1) / kCkptWarps;
+  const int grid = static_cast<int>(b < 148 * per ? b : 148 * per);
+  return launch_kernel(norm_ckpt_kernel, dim3(grid), dim3(kCkptWarps * 32), smem, st, h, g, eps, T, d,
+                       x, q, scales, rstd);
 }
 
 size_t rms_norm_backward_scratch_bytes(int T, int d) {
@@ -241,13 +389,14 @@ cudaError_t launch_rms_norm_backward(const uint16_t* dx, const uint16_t* h, cons
                          mask, T, d, dh_in, dh, partial);
   };
   cudaError_t e;
-  if (q)
-    e = s.chunks == 1 ? go(norm_backward_kernel<true, 1>) : go(norm_backward_kernel<true, 2>);
-  else
-    e = s.chunks == 1 ? go(norm_backward_kernel<false, 1>) : go(norm_backward_kernel<false, 2>);
+  switch (s.chunks) {
+    case 1: e = q ? go(norm_backward_kernel<true, 1>) : go(norm_backward_kernel<false, 1>); break;
+    case 2: e = q ? go(norm_backward_kernel<true, 2>) : go(norm_backward_kernel<false, 2>); break;
+    default: e = q ? go(norm_backward_kernel<true, 4>) : go(norm_backward_kernel<false, 4>);
+  }
   if (e != cudaSuccess) return e;
   pdl_launches() = true;
-  return launch_kernel(norm_dg_kernel, dim3(d / 32), dim3(256), 0, st, partial, s.blocks, d,
+  return launch_kernel(norm_dg_kernel, dim3(d / 32), dim3(1024), 0, st, partial, s.blocks, d,
                        accumulate, dg);
 }
 
