@@ -504,6 +504,16 @@ MOE_API int moe_forward_launch_count(int E, int k, int T, int d, int I);
  *   left out of every sum and count, and none of its floating-point inputs
  *   (logits, rows, gradients) changes a result, whatever they hold.
  * - accumulate (0 or 1): add to the output instead of overwriting it.
+ * - A workspace needs no initialisation and may be shared by calls that run one
+ *   after another. Its first word is moe_router_backward's status (0, or
+ *   MOE_ERR_TIMEOUT if one of its bounded waits gave up: moe_sync_status); no
+ *   other call writes it.
+ * - A call reads and writes nothing but its arguments: calls on different
+ *   streams with workspaces of their own may run at the same time, and each may
+ *   be captured into a CUDA graph.
+ * - A NaN or an infinity in a live token's inputs shows as NaN (or infinity) in
+ *   the outputs that depend on it; a logits' gradient beyond bf16's largest value
+ *   (3.39e38) counts as an infinity in moe_router_backward.
  * - Every sum over tokens has a fixed order: the same call gives the same bits.
  */
 

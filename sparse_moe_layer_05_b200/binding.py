@@ -607,10 +607,48 @@ def moe_selftest_wait_timeout(workspace, stream=None) -> None:
 
 # ----------------------------------------------------------- convenience ----
 
+class NormCheckpoint:
+    """What moe_forward_block_checkpoint leaves of its norm's input: E4M3 codes,
+    E8M0 scales and the rows' inverse roots, for up to T tokens."""
+
+    def __init__(self, T: int, d: int, device="cuda"):
+        import torch
+        self.q = torch.empty((T, d), dtype=torch.uint8, device=device)
+        self.scales = torch.empty((T, d // 32), dtype=torch.uint8, device=device)
+        self.rstd = torch.empty(T, dtype=torch.float32, device=device)
+
+    def rows(self, T: int):
+        return self.q[:T], self.scales[:T], self.rstd[:T]
+
+
+class RouterGrads:
+    """Gradients of a layer's router and norm (dW_r, db_r, dg), the auxiliary loss's
+    values (stats: loss, balance, z, live tokens; counts; mean_probs), and the
+    buffers and workspace that MoELayer.backward_block uses, for up to T tokens."""
+
+    def __init__(self, E: int, k: int, T: int, d: int, device="cuda"):
+        import torch
+        f = lambda *s: torch.zeros(s, dtype=torch.float32, device=device)
+        self.T = T
+        self.dW_r, self.db_r, self.dg = f(E, d), f(E), f(d)
+        self.stats, self.mean_probs = f(4), f(E)
+        self.counts = torch.zeros(E, dtype=torch.int32, device=device)
+        self.dlogits, self.lse = f(T, E), f(T)
+        self.dx = torch.empty((T, d), dtype=torch.uint16, device=device)
+        # the calls run one after another, so they share the largest one's workspace
+        nbytes = max(moe_balance_loss_workspace_size(E, k, T),
+                     moe_router_backward_workspace_size(E, T, d),
+                     moe_rms_norm_backward_workspace_size(T, d))
+        if nbytes == 0:
+            raise ValueError("unsupported shape")
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 class MoELayer:
     """Device-resident MoE layer: weights uploaded once, workspace owned here."""
 
-    def __init__(self, inp, device="cuda", T_max: Optional[int] = None, hostio: bool = False):
+    def __init__(self, inp, device="cuda", T_max: Optional[int] = None, hostio: bool = False,
+                 block: bool = False):
         import torch
         self.d, self.I, self.E, self.k = inp.d, inp.I, inp.E, inp.k
         to = lambda a: torch.from_numpy(a).to(device)
@@ -621,7 +659,8 @@ class MoELayer:
         self.Wd_codes = to(inp.Wd_codes)
         self.Wd_scales = to(inp.Wd_scales)
         self.T_max = T_max if T_max is not None else inp.T
-        size_fn = moe_workspace_size_hostio if hostio else moe_workspace_size
+        size_fn = (moe_workspace_size_hostio if hostio else
+                   moe_workspace_size_block if block else moe_workspace_size)
         nbytes = size_fn(self.E, self.k, self.T_max, self.d, self.I)
         if nbytes == 0:
             raise ValueError("unsupported shape")
@@ -637,6 +676,58 @@ class MoELayer:
         moe_forward(x, self.W_r, self.b_r, self.Wgu_codes, self.Wgu_scales, self.Wd_codes,
                     self.Wd_scales, self.E, self.k, T, self.d, self.I, out, self.workspace, stream)
         return out
+
+    def forward_block(self, h, g, eps: float, out=None, checkpoint: Optional[NormCheckpoint] = None,
+                      stream=None):
+        """out = h + MoE(RMSNorm(h)) (a layer made with block=True); with a
+        checkpoint, the training form, whose backward pass is backward_block."""
+        import torch
+        T = h.shape[0]
+        if T > self.T_max:
+            raise ValueError("more tokens than the workspace was sized for")
+        if out is None:
+            out = torch.empty((T, self.d), dtype=torch.uint16, device=h.device)
+        args = (h, g, eps, self.W_r, self.b_r, self.Wgu_codes, self.Wgu_scales, self.Wd_codes,
+                self.Wd_scales, self.E, self.k, T, self.d, self.I, out)
+        if checkpoint is None:
+            moe_forward_block(*args, self.workspace, stream)
+        else:
+            moe_forward_block_checkpoint(*args, *checkpoint.rows(T), self.workspace, stream)
+        return out
+
+    def backward_block(self, dout, g, checkpoint: NormCheckpoint, grads: RouterGrads,
+                       balance_coef: float = 0.0, z_coef: float = 0.0, dloss=None, dx_in=None,
+                       token_mask=None, accumulate: bool = False, dh=None, stream=None):
+        """The backward pass of forward_block with a checkpoint, right after it (what
+        it reads lies in the layer's workspace): fills grads from dout bf16 [T, d],
+        the gradient of out, and returns dh bf16 [T, d]. The auxiliary loss
+        balance_coef * balance + z_coef * z is weighted by dloss (f32 [1]; None: 1).
+        The experts are frozen; their share of the gradient that reaches
+        RMSNorm(h), if the caller has it, is dx_in bf16 [T, d]."""
+        import torch
+        T = dout.shape[0]
+        if T > grads.T:
+            raise ValueError("more tokens than the gradients' buffers were sized for")
+        if dh is None:
+            dh = torch.empty((T, self.d), dtype=torch.uint16, device=dout.device)
+        E, k, d, mask = self.E, self.k, self.d, token_mask
+        logits, idx = self.intermediate("logits", T), self.intermediate("topk_idx", T)
+        dlogits, dx, ws = grads.dlogits[:T], grads.dx[:T], grads.workspace
+        q, scales, rstd = checkpoint.rows(T)
+        moe_gate_backward(dout, self.intermediate("yw", T), idx, self.intermediate("topk_w", T), E, k,
+                          T, d, dlogits, token_mask=mask, stream=stream)
+        moe_balance_loss(logits, idx, E, k, T, balance_coef, z_coef, grads.stats, grads.counts,
+                         grads.mean_probs, grads.lse[:T], ws, token_mask=mask, stream=stream)
+        if balance_coef or z_coef:
+            moe_balance_loss_backward(logits, grads.lse[:T], grads.counts, grads.stats, E, k, T,
+                                      balance_coef, z_coef, dlogits, dloss=dloss, token_mask=mask,
+                                      accumulate=True, stream=stream)
+        moe_router_backward(dlogits, self.W_r, E, T, d, grads.dW_r, grads.db_r, dx, ws, q=q,
+                            scales=scales, rstd=rstd, g=g, dx_in=dx_in, token_mask=mask,
+                            accumulate=accumulate, stream=stream)
+        moe_rms_norm_backward(dx, g, rstd, T, d, dh, grads.dg, ws, q=q, scales=scales, dh_in=dout,
+                              token_mask=mask, accumulate=accumulate, stream=stream)
+        return dh
 
     def forward_timed(self, x, out, stream=None):
         T = x.shape[0]

@@ -1059,10 +1059,13 @@ moe_status moe_selftest_wait_timeout(void* workspace_dev, void* stream) {
 }
 
 // ---------------------------------------------------- training the router ----
+// Every workspace of these calls begins with the status block, which only
+// moe_router_backward writes: the calls of a backward pass may share one.
+static constexpr size_t kTrainStatus = 256;
 
 size_t moe_balance_loss_workspace_size(int E, int k, int T) {
   if (!shape_ok(E, k, T, 32)) return 0;
-  return moe::balance_scratch_bytes(E, T);
+  return kTrainStatus + moe::balance_scratch_bytes(E, T);
 }
 
 moe_status moe_balance_loss(const float* logits_dev, const int32_t* topk_idx_dev,
@@ -1077,14 +1080,15 @@ moe_status moe_balance_loss(const float* logits_dev, const int32_t* topk_idx_dev
                       mean_probs_dev, lse_dev, workspace_dev}))
     return MOE_ERR_INVALID_ARG;
   if (!shape_ok(E, k, T, 32)) return MOE_ERR_UNSUPPORTED;
-  if (workspace_bytes < moe::balance_scratch_bytes(E, T)) return MOE_ERR_WORKSPACE;
+  if (workspace_bytes < kTrainStatus + moe::balance_scratch_bytes(E, T)) return MOE_ERR_WORKSPACE;
   int num_sms = 0;
   moe_status s = device_info(&num_sms);
   if (s != MOE_OK) return s;
   PdlPass pdl_pass;
   MOE_CUDA(moe::launch_balance_loss(logits_dev, topk_idx_dev, token_mask_dev, E, k, T, balance_coef,
                                     z_coef, stats_dev, counts_dev, mean_probs_dev, lse_dev,
-                                    workspace_dev, static_cast<cudaStream_t>(stream)));
+                                    at<void>(workspace_dev, kTrainStatus),
+                                    static_cast<cudaStream_t>(stream)));
   return MOE_OK;
 }
 
@@ -1133,7 +1137,7 @@ moe_status moe_gate_backward(const void* dout_dev, const float* yw_dev, const in
 
 size_t moe_router_backward_workspace_size(int E, int T, int d) {
   if (!shape_ok(E, 1, T, d)) return 0;
-  return align256(16) + moe::router_grad_scratch_bytes(E, T, d);
+  return kTrainStatus + moe::router_grad_scratch_bytes(E, T, d);
 }
 
 moe_status moe_router_backward(const float* dlogits_dev, const float* W_r_dev, const void* x_dev,
@@ -1178,7 +1182,7 @@ moe_status moe_router_backward(const float* dlogits_dev, const float* W_r_dev, c
   p.db = db_dev;
   p.dx = static_cast<uint16_t*>(dx_dev);
   p.status = static_cast<int*>(workspace_dev);
-  p.scratch = at<void>(workspace_dev, align256(16));
+  p.scratch = at<void>(workspace_dev, kTrainStatus);
   PdlPass pdl_pass;
   MOE_CUDA(moe::launch_router_backward(p, static_cast<cudaStream_t>(stream)));
   return MOE_OK;
@@ -1205,7 +1209,7 @@ moe_status moe_rms_norm_checkpoint(const void* h_dev, const float* g_dev, float 
 
 size_t moe_rms_norm_backward_workspace_size(int T, int d) {
   if (!shape_ok(1, 1, T, d)) return 0;
-  return moe::rms_norm_backward_scratch_bytes(T, d);
+  return kTrainStatus + moe::rms_norm_backward_scratch_bytes(T, d);
 }
 
 moe_status moe_rms_norm_backward(const void* dx_dev, const void* h_dev, const uint8_t* q_dev,
@@ -1224,7 +1228,8 @@ moe_status moe_rms_norm_backward(const void* dx_dev, const void* h_dev, const ui
                       dh_dev, dg_dev, workspace_dev}))
     return MOE_ERR_INVALID_ARG;
   if (!shape_ok(1, 1, T, d)) return MOE_ERR_UNSUPPORTED;
-  if (workspace_bytes < moe::rms_norm_backward_scratch_bytes(T, d)) return MOE_ERR_WORKSPACE;
+  if (workspace_bytes < kTrainStatus + moe::rms_norm_backward_scratch_bytes(T, d))
+    return MOE_ERR_WORKSPACE;
   int num_sms = 0;
   moe_status s = device_info(&num_sms);
   if (s != MOE_OK) return s;
@@ -1232,7 +1237,7 @@ moe_status moe_rms_norm_backward(const void* dx_dev, const void* h_dev, const ui
   MOE_CUDA(moe::launch_rms_norm_backward(
       static_cast<const uint16_t*>(dx_dev), static_cast<const uint16_t*>(h_dev), q_dev, scales_dev,
       rstd_dev, g_dev, token_mask_dev, T, d, static_cast<const uint16_t*>(dh_in_dev),
-      accumulate != 0, static_cast<uint16_t*>(dh_dev), dg_dev, workspace_dev,
+      accumulate != 0, static_cast<uint16_t*>(dh_dev), dg_dev, at<void>(workspace_dev, kTrainStatus),
       static_cast<cudaStream_t>(stream)));
   return MOE_OK;
 }
