@@ -38,80 +38,162 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 // -------------------------------------------------------- balance loss ----
-// Two launches: one warp per token in blocks of up to 32 warps, whose sums are
-// joined in shared memory, so that the second launch, one block, has at most 148
-// rows of sums to add (in fp64).
+// One warp per token; a block's sums are joined in shared memory and those of a
+// cluster of four blocks over its shared memory, so that the finishing block has
+// at most 32 rows of sums to add (in fp64): with a row per block it took longer
+// than the pass over the logits. 32 clusters, because 36 do not fit the device at
+// once (T = 16384, E = 128: 11 us against 16 in two waves). A batch that one cluster
+// holds is finished in the same launch.
 
 constexpr int kMaxE = 256;
-constexpr int kBalBlocks = 148, kBalWarps = 32;
+constexpr int kBalCluster = 4, kBalClusters = 32, kBalWarps = 32;
+constexpr int kBalOneCluster = 256;   // tokens: two per warp
 
-// Warps of a block and blocks: one token per warp as long as the blocks last.
+// Warps of a block and clusters: one token per warp as long as the blocks last.
 int balance_warps(int T) {
-  const int w = (T + kBalBlocks - 1) / kBalBlocks;
+  const int blocks = T <= kBalOneCluster ? kBalCluster : kBalCluster * kBalClusters;
+  const int w = T / blocks + (T % blocks != 0);
   return w < 4 ? 4 : w > kBalWarps ? kBalWarps : w;
 }
-int balance_blocks(int T) {
-  const int w = balance_warps(T);
-  const int64_t b = (static_cast<int64_t>(T) + w - 1) / w;
-  return b < 1 ? 1 : b > kBalBlocks ? kBalBlocks : static_cast<int>(b);
+int balance_clusters(int T) {
+  if (T <= kBalOneCluster) return 1;
+  const int per = balance_warps(T) * kBalCluster;
+  const int c = T / per + (T % per != 0);
+  return c > kBalClusters ? kBalClusters : c;
 }
 
-// Per block: sums over its tokens of p[e] and lse^2, the counts, live tokens.
+// Per cluster: sums over its tokens of p[e] and lse^2, the counts, live tokens.
 struct BalanceScratch {
-  float* p;        // [blocks][E]
-  int32_t* counts; // [blocks][E]
-  double* z;       // [blocks]
-  int32_t* n;      // [blocks]
+  float* p;        // [clusters][E]
+  int32_t* counts; // [clusters][E]
+  double* z;       // [clusters]
+  int32_t* n;      // [clusters]
 };
 
-BalanceScratch balance_scratch(void* base, int E, int blocks) {
+BalanceScratch balance_scratch(void* base, int E, int clusters) {
   BalanceScratch s;
   uint8_t* b = static_cast<uint8_t*>(base);
   s.z = reinterpret_cast<double*>(b);
-  b += static_cast<size_t>(kBalBlocks) * 8;
+  b += static_cast<size_t>(kBalClusters) * 8;
   s.n = reinterpret_cast<int32_t*>(b);
-  b += static_cast<size_t>(kBalBlocks) * 4;
+  b += static_cast<size_t>(kBalClusters) * 4;
   s.p = reinterpret_cast<float*>(b);
-  b += static_cast<size_t>(blocks) * E * 4;
+  b += static_cast<size_t>(clusters) * E * 4;
   s.counts = reinterpret_cast<int32_t*>(b);
   return s;
 }
 
-// One warp per token, lane l holding logits l, l + 32, ...; the next token's
-// logits are loaded while this one's are summed.
+struct BalanceOut {
+  float balance_coef, z_coef;
+  float* stats;        // [4]
+  int32_t* counts;     // [E]
+  float* mean_probs;   // [E]
+};
+
+// A lane's NL (4 for at most 128 experts, else 8) of a row's experts: four
+// neighbours at a time where rows are whole float4s (VEC), else lane, lane + 32, ...
+template <bool VEC>
+__device__ __forceinline__ int expert_of(int lane, int i) {
+  return VEC ? 4 * lane + (i & 3) + 128 * (i >> 2) : lane + 32 * i;
+}
+template <bool VEC, int NL>
+__device__ __forceinline__ void load_row(const float* row, int E, int lane, float (&v)[NL]) {
+  if (VEC) {
+#pragma unroll
+    for (int h = 0; h < NL / 4; ++h) {
+      const int e = 4 * lane + 128 * h;
+      const float4 x = e < E ? __ldg(reinterpret_cast<const float4*>(row + e))
+                             : make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F);
+      v[4 * h] = x.x;
+      v[4 * h + 1] = x.y;
+      v[4 * h + 2] = x.z;
+      v[4 * h + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) v[i] = lane + 32 * i < E ? __ldg(row + lane + 32 * i) : -CUDART_INF_F;
+  }
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
+  double v;
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// The loss from all sums: thread e < E has expert e's, z and n are the block's.
+// Whole block (at least E threads, whole warps); red: 32 doubles of shared memory.
+__device__ __forceinline__ void balance_results(double p, int c, double z, int n, int E, int k,
+                                                const BalanceOut& o, double* red) {
+  const int e = threadIdx.x;
+  double term = 0.0;
+  if (e < E) {
+    const double mean = n > 0 ? p / n : 0.0;
+    o.counts[e] = c;
+    o.mean_probs[e] = static_cast<float>(mean);
+    term = n > 0 ? mean * (static_cast<double>(c) / (static_cast<double>(n) * k)) : 0.0;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) term += __shfl_xor_sync(0xFFFFFFFFu, term, off);
+  if ((e & 31) == 0) red[e >> 5] = term;
+  __syncthreads();
+  if (e == 0) {
+    double bal = 0.0;
+    for (int w = 0; w < (E + 31) / 32; ++w) bal += red[w];
+    bal *= E;
+    const double zz = n > 0 ? z / n : 0.0;
+    o.stats[0] = static_cast<float>(o.balance_coef * bal + o.z_coef * zz);
+    o.stats[1] = static_cast<float>(bal);
+    o.stats[2] = static_cast<float>(zz);
+    o.stats[3] = static_cast<float>(n);
+  }
+}
+
+// The next token's logits are loaded while this one's are summed. clusters == 1:
+// the results too (at least E threads per block).
+template <bool VEC, int NL>
 __global__ void __launch_bounds__(kBalWarps * 32) balance_partial_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ idx,
-    const uint8_t* __restrict__ mask, int E, int k, int T, float* __restrict__ lse_out,
-    BalanceScratch sc) {
+    const uint8_t* __restrict__ mask, int E, int k, int T, int clusters,
+    float* __restrict__ lse_out, BalanceScratch sc, BalanceOut out) {
   pdl_wait_and_trigger();
   __shared__ float sp[kBalWarps][kMaxE];
-  __shared__ int sc_cnt[kMaxE];
-  __shared__ double sz[kBalWarps];
-  __shared__ int sn[kBalWarps];
+  __shared__ float bp[kMaxE];              // the block's sums
+  __shared__ int bc[kMaxE];
+  __shared__ double sz[kBalWarps], bz, red[32];
+  __shared__ int sn[kBalWarps], bn;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  for (int e = threadIdx.x; e < E; e += blockDim.x) sc_cnt[e] = 0;
+  for (int e = threadIdx.x; e < E; e += blockDim.x) bc[e] = 0;
   __syncthreads();
-  float acc[8], next[8];
+  float acc[NL], next[NL];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  double z = 0.0;
+  for (int i = 0; i < NL; ++i) acc[i] = 0.f;
+  float z = 0.f;
   int n = 0, next_idx = -1;
   uint32_t next_live = 1;
   const int64_t step = static_cast<int64_t>(gridDim.x) * warps;
   auto load = [&](int64_t t) {
     if (t >= T) return;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      next[i] = lane + 32 * i < E ? __ldg(logits + t * E + lane + 32 * i) : -CUDART_INF_F;
+    load_row<VEC, NL>(logits + t * E, E, lane, next);
     next_idx = lane < k ? __ldg(idx + t * k + lane) : -1;   // k is at most 32
     if (mask) next_live = __ldg(mask + t);
   };
   int64_t t = static_cast<int64_t>(blockIdx.x) * warps + warp;
   load(t);
   for (; t < T; t += step) {
-    float v[8];
+    float v[NL];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = next[i];
+    for (int i = 0; i < NL; ++i) v[i] = next[i];
     const int chosen = next_idx;
     const bool live = next_live != 0;
     load(t + step);
@@ -120,31 +202,32 @@ __global__ void __launch_bounds__(kBalWarps * 32) balance_partial_kernel(
       continue;
     }
     ++n;
-    float m = -CUDART_INF_F;
+    // the maximum leaves NaNs out; they reach the sum through their own term
+    float m = v[0];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = v[i] > m || v[i] != v[i] ? v[i] : m;   // keeps a NaN
-    const bool nan = __any_sync(0xFFFFFFFFu, m != m);
+    for (int i = 1; i < NL; ++i) m = fmaxf(m, v[i]);
     m = warp_max(m);
+    const float base = m == -CUDART_INF_F ? 0.f : m;   // places past E hold -inf: exp gives 0
     float sum = 0.f;
-    const bool none = m == -CUDART_INF_F && !nan;   // every logit is -inf
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = lane + 32 * i < E && !none ? expf(v[i] - m) : 0.f;
+    for (int i = 0; i < NL; ++i) {
+      v[i] = expf(v[i] - base);
       sum += v[i];
     }
     sum = warp_sum(sum);
-    const float l = none ? -CUDART_INF_F : m + logf(sum);
+    const bool none = sum == 0.f;                      // every logit is -inf
+    const float l = none ? -CUDART_INF_F : base + logf(sum);
     const float inv = none ? 0.f : 1.f / sum;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] += v[i] * inv;
+    for (int i = 0; i < NL; ++i) acc[i] += v[i] * inv;
     if (lane == 0) {
       lse_out[t] = l;
-      if (!none) z += static_cast<double>(l) * l;
+      if (!none) z = fmaf(l, l, z);
     }
-    if (static_cast<unsigned>(chosen) < static_cast<unsigned>(E)) atomicAdd(&sc_cnt[chosen], 1);
+    if (static_cast<unsigned>(chosen) < static_cast<unsigned>(E)) atomicAdd(&bc[chosen], 1);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sp[warp][lane + 32 * i] = acc[i];
+  for (int i = 0; i < NL; ++i) sp[warp][expert_of<VEC>(lane, i)] = acc[i];
   if (lane == 0) {
     sz[warp] = z;
     sn[warp] = n;
@@ -152,103 +235,109 @@ __global__ void __launch_bounds__(kBalWarps * 32) balance_partial_kernel(
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     float s = 0.f;
+#pragma unroll 4
     for (int w = 0; w < warps; ++w) s += sp[w][e];
-    sc.p[static_cast<size_t>(blockIdx.x) * E + e] = s;
-    sc.counts[static_cast<size_t>(blockIdx.x) * E + e] = sc_cnt[e];
+    bp[e] = s;
   }
-  if (threadIdx.x == 0) {
-    double zz = 0.0;
-    int nn = 0;
-    for (int w = 0; w < warps; ++w) {
-      zz += sz[w];
-      nn += sn[w];
-    }
-    sc.z[blockIdx.x] = zz;
-    sc.n[blockIdx.x] = nn;
-  }
-}
-
-// cols: E rounded up to a power of two; thread (share, e) adds every
-// (1024 / cols)-th block's row.
-__global__ void __launch_bounds__(1024) balance_finish_kernel(BalanceScratch sc, int blocks, int E,
-                                                              int cols, int k, float balance_coef,
-                                                              float z_coef, float* stats,
-                                                              int32_t* counts, float* mean_probs) {
-  pdl_wait_and_trigger();
-  __shared__ double sp[1024];
-  __shared__ int scnt[1024];
-  __shared__ double s_z;
-  __shared__ int s_n;
-  const int e = threadIdx.x & (cols - 1), share = threadIdx.x / cols, shares = 1024 / cols;
-  double p = 0.0;
-  int c = 0;
-  if (e < E) {
-    // eight rows at a time: all their loads before the sums
-    for (int b0 = share; b0 < blocks; b0 += 8 * shares) {
-      float pv[8];
-      int cv[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int b = b0 + i * shares;
-        pv[i] = b < blocks ? __ldg(sc.p + static_cast<size_t>(b) * E + e) : 0.f;
-        cv[i] = b < blocks ? __ldg(sc.counts + static_cast<size_t>(b) * E + e) : 0;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        p += pv[i];
-        c += cv[i];
-      }
-    }
-  }
-  sp[threadIdx.x] = p;
-  scnt[threadIdx.x] = c;
-  if (threadIdx.x < 32) {
-    double z = 0.0;
-    int n = 0;
-    for (int b = threadIdx.x; b < blocks; b += 32) {
-      z += sc.z[b];
-      n += sc.n[b];
-    }
+  if (warp == 0) {
+    double zz = lane < warps ? sz[lane] : 0.0;
+    int nn = lane < warps ? sn[lane] : 0;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
-      z += __shfl_xor_sync(0xFFFFFFFFu, z, off);
-      n += __shfl_xor_sync(0xFFFFFFFFu, n, off);
+      zz += __shfl_xor_sync(0xFFFFFFFFu, zz, off);
+      nn += __shfl_xor_sync(0xFFFFFFFFu, nn, off);
     }
-    if (threadIdx.x == 0) {
-      s_z = z;
-      s_n = n;
+    if (lane == 0) {
+      bz = zz;
+      bn = nn;
     }
   }
   __syncthreads();
-  const int n = s_n;
-  double term = 0.0;
-  if (threadIdx.x < E) {   // share 0
+  cluster_sync();
+  // over the cluster's blocks in order: every block a share of the experts, or
+  // block 0 all of them where it goes on to the results
+  const uint32_t rank = cluster_ctarank();
+  const bool one = clusters == 1;
+  const int cluster = blockIdx.x / kBalCluster;
+  if (!one || rank == 0) {
+    const int e = one ? threadIdx.x : threadIdx.x * kBalCluster + static_cast<int>(rank);
+    float s[kBalCluster];
+    int c[kBalCluster];
+    double p = 0.0, zz = 0.0;
+    int cnt = 0, nn = 0;
+    if (e < E) {
+#pragma unroll
+      for (int r = 0; r < kBalCluster; ++r) {
+        s[r] = ld_cluster_f32(mapa_shared(smem_u32(&bp[e]), r));
+        c[r] = ld_cluster_s32(mapa_shared(smem_u32(&bc[e]), r));
+      }
+#pragma unroll
+      for (int r = 0; r < kBalCluster; ++r) {
+        p += s[r];
+        cnt += c[r];
+      }
+    }
+    if (one || threadIdx.x == 0)
+#pragma unroll
+      for (int r = 0; r < kBalCluster; ++r) {
+        zz += ld_cluster_f64(mapa_shared(smem_u32(&bz), r));
+        nn += ld_cluster_s32(mapa_shared(smem_u32(&bn), r));
+      }
+    if (one) {
+      balance_results(p, cnt, zz, nn, E, k, out, red);
+    } else {
+      if (e < E) {
+        sc.p[static_cast<size_t>(cluster) * E + e] = static_cast<float>(p);
+        sc.counts[static_cast<size_t>(cluster) * E + e] = cnt;
+      }
+      if (rank == 0 && threadIdx.x == 0) {
+        sc.z[cluster] = zz;
+        sc.n[cluster] = nn;
+      }
+    }
+  }
+  cluster_sync();   // no block leaves while another reads its sums
+}
+
+// cols: E rounded up to a power of two; thread (share, e) adds every
+// (1024 / cols)-th cluster's row, at most nine.
+__global__ void __launch_bounds__(1024) balance_finish_kernel(BalanceScratch sc, int clusters, int E,
+                                                              int cols, int k, BalanceOut out) {
+  pdl_wait_and_trigger();
+  __shared__ double sp[1024], red[32];
+  __shared__ int scnt[1024];
+  const int e = threadIdx.x & (cols - 1), share = threadIdx.x / cols, shares = 1024 / cols;
+  double p = 0.0, z = 0.0;
+  int c = 0, n = 0;
+  if (e < E) {
+    for (int b = share; b < clusters; b += shares) {
+      p += __ldg(sc.p + static_cast<size_t>(b) * E + e);
+      c += __ldg(sc.counts + static_cast<size_t>(b) * E + e);
+    }
+  }
+  // every warp: z and n of all clusters
+  const int lane = threadIdx.x & 31;
+  for (int b = lane; b < clusters; b += 32) {
+    z += __ldg(sc.z + b);
+    n += __ldg(sc.n + b);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    z += __shfl_xor_sync(0xFFFFFFFFu, z, off);
+    n += __shfl_xor_sync(0xFFFFFFFFu, n, off);
+  }
+  sp[threadIdx.x] = p;
+  scnt[threadIdx.x] = c;
+  __syncthreads();
+  if (share == 0)
     for (int s = 1; s < shares; ++s) {
       p += sp[s * cols + e];
       c += scnt[s * cols + e];
     }
-    const double mean = n > 0 ? p / n : 0.0;
-    counts[e] = c;
-    mean_probs[e] = static_cast<float>(mean);
-    term = n > 0 ? mean * (static_cast<double>(c) / (static_cast<double>(n) * k)) : 0.0;
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) term += __shfl_xor_sync(0xFFFFFFFFu, term, off);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sp[threadIdx.x >> 5] = term;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double bal = 0.0;
-    for (int w = 0; w < (E + 31) / 32; ++w) bal += sp[w];
-    bal *= E;
-    const double z = n > 0 ? s_z / n : 0.0;
-    stats[0] = static_cast<float>(balance_coef * bal + z_coef * z);
-    stats[1] = static_cast<float>(bal);
-    stats[2] = static_cast<float>(z);
-    stats[3] = static_cast<float>(n);
-  }
+  balance_results(p, c, z, n, E, k, out, red);
 }
 
+template <bool VEC, int NL>
 __global__ void __launch_bounds__(256) balance_backward_kernel(
     const float* __restrict__ logits, const float* __restrict__ lse,
     const int32_t* __restrict__ counts, const float* __restrict__ stats,
@@ -256,37 +345,61 @@ __global__ void __launch_bounds__(256) balance_backward_kernel(
     const float* __restrict__ dloss, bool accumulate, float* dlogits) {
   pdl_wait_and_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float n = stats[3];
-  const float scale = n > 0.f ? (dloss ? dloss[0] : 1.f) / n : 0.f;
-  float f[8];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + warp;
+  if (t >= T) return;
+  // the first token's row and everything that does not depend on the token at once
+  float v[NL], l = __ldg(lse + t), f[NL];
+  uint32_t live_byte = mask ? __ldg(mask + t) : 1u;
+  load_row<VEC, NL>(logits + t * E, E, lane, v);
+  const float n = __ldg(stats + 3), up = dloss ? __ldg(dloss) : 1.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = lane + 32 * i;
-    f[i] = e < E && n > 0.f ? static_cast<float>(counts[e]) / (n * (float)k) : 0.f;
+  for (int i = 0; i < NL; ++i) {
+    const int e = expert_of<VEC>(lane, i);
+    f[i] = e < E ? static_cast<float>(__ldg(counts + e)) : 0.f;
   }
-  for (int t = blockIdx.x * 8 + warp; t < T; t += gridDim.x * 8) {
-    const float l = lse[t];
-    const bool live = (!mask || mask[t] != 0) && l != -CUDART_INF_F;
-    float p[8];
-    float fp = 0.f;
+  const float scale = n > 0.f ? up / n : 0.f, per = n > 0.f ? 1.f / (n * static_cast<float>(k)) : 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = lane + 32 * i;
-      p[i] = live && e < E ? expf(__ldg(logits + (size_t)t * E + e) - l) : 0.f;
+  for (int i = 0; i < NL; ++i) f[i] *= per;
+  const float aE = balance_coef * static_cast<float>(E);
+  for (; t < T; t += step) {
+    const bool live = live_byte != 0 && l != -CUDART_INF_F;
+    const float lt = l;
+    float p[NL], fp = 0.f;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      p[i] = live && expert_of<VEC>(lane, i) < E ? expf(v[i] - lt) : 0.f;
       fp = fmaf(f[i], p[i], fp);
     }
+    if (t + step < T) {
+      l = __ldg(lse + t + step);
+      if (mask) live_byte = __ldg(mask + t + step);
+      load_row<VEC, NL>(logits + (t + step) * E, E, lane, v);
+    }
     fp = warp_sum(fp);
+    if (!live && accumulate) continue;   // left alone
+    const float zt = 2.f * z_coef * lt;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = lane + 32 * i;
-      if (e >= E) continue;
-      const float v = live ? scale * p[i] * (balance_coef * (float)E * (f[i] - fp) + 2.f * z_coef * l)
-                           : 0.f;
-      float* o = dlogits + (size_t)t * E + e;
-      if (live)
-        *o = accumulate ? *o + v : v;
-      else if (!accumulate)
-        *o = 0.f;
+    for (int i = 0; i < NL; ++i) p[i] = live ? scale * p[i] * (aE * (f[i] - fp) + zt) : 0.f;
+    float* row = dlogits + t * E;
+    if (VEC) {
+#pragma unroll
+      for (int h = 0; h < NL / 4; ++h) {
+        const int e = 4 * lane + 128 * h;
+        if (e >= E) continue;
+        float4 o = make_float4(p[4 * h], p[4 * h + 1], p[4 * h + 2], p[4 * h + 3]);
+        if (accumulate) {
+          const float4 b = *reinterpret_cast<const float4*>(row + e);
+          o = make_float4(o.x + b.x, o.y + b.y, o.z + b.z, o.w + b.w);
+        }
+        *reinterpret_cast<float4*>(row + e) = o;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int e = lane + 32 * i;
+        if (e < E) row[e] = accumulate ? row[e] + p[i] : p[i];
+      }
     }
   }
 }
@@ -531,23 +644,30 @@ constexpr int kSmallTokens = 128;
 }  // namespace
 
 size_t balance_scratch_bytes(int E, int T) {
-  return static_cast<size_t>(kBalBlocks) * 12 + static_cast<size_t>(balance_blocks(T)) * E * 8;
+  return static_cast<size_t>(kBalClusters) * 12 + static_cast<size_t>(balance_clusters(T)) * E * 8;
 }
 
 cudaError_t launch_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask,
                                 int E, int k, int T, float balance_coef, float z_coef,
                                 float* stats, int32_t* counts, float* mean_probs, float* lse,
                                 void* scratch, cudaStream_t st) {
-  const int blocks = balance_blocks(T);
-  const BalanceScratch sc = balance_scratch(scratch, E, blocks);
-  cudaError_t e = launch_kernel(balance_partial_kernel, dim3(blocks), dim3(balance_warps(T) * 32), 0,
-                                st, logits, topk_idx, mask, E, k, T, lse, sc);
-  if (e != cudaSuccess) return e;
+  const int clusters = balance_clusters(T);
+  const BalanceScratch sc = balance_scratch(scratch, E, clusters);
+  const BalanceOut out{balance_coef, z_coef, stats, counts, mean_probs};
+  int warps = balance_warps(T);
+  if (warps * 32 < E) warps = (E + 31) / 32;   // a thread per expert
+  auto go = [&](auto kernel) {
+    return launch_kernel_cluster(kernel, dim3(clusters * kBalCluster), dim3(warps * 32), 0, kBalCluster,
+                                 st, logits, topk_idx, mask, E, k, T, clusters, lse, sc, out);
+  };
+  const cudaError_t e = E % 4 == 0
+                            ? (E <= 128 ? go(balance_partial_kernel<true, 4>) : go(balance_partial_kernel<true, 8>))
+                            : (E <= 128 ? go(balance_partial_kernel<false, 4>) : go(balance_partial_kernel<false, 8>));
+  if (e != cudaSuccess || clusters == 1) return e;
   pdl_launches() = true;
   int cols = 32;
   while (cols < E) cols *= 2;
-  return launch_kernel(balance_finish_kernel, dim3(1), dim3(1024), 0, st, sc, blocks, E, cols, k,
-                       balance_coef, z_coef, stats, counts, mean_probs);
+  return launch_kernel(balance_finish_kernel, dim3(1), dim3(1024), 0, st, sc, clusters, E, cols, k, out);
 }
 
 cudaError_t launch_balance_backward(const float* logits, const float* lse, const int32_t* counts,
@@ -555,9 +675,13 @@ cudaError_t launch_balance_backward(const float* logits, const float* lse, const
                                     float balance_coef, float z_coef, const float* dloss,
                                     bool accumulate, float* dlogits, cudaStream_t st) {
   const int64_t b = (static_cast<int64_t>(T) + 7) / 8;
-  return launch_kernel(balance_backward_kernel, dim3(b < 148 * 8 ? static_cast<int>(b) : 148 * 8),
-                       dim3(256), 0, st, logits, lse, counts, stats, mask, E, k, T, balance_coef,
-                       z_coef, dloss, accumulate, dlogits);
+  const dim3 grid(b < 148 * 8 ? static_cast<int>(b) : 148 * 8);
+  auto go = [&](auto kernel) {
+    return launch_kernel(kernel, grid, dim3(256), 0, st, logits, lse, counts, stats, mask, E, k, T,
+                         balance_coef, z_coef, dloss, accumulate, dlogits);
+  };
+  if (E % 4 == 0) return E <= 128 ? go(balance_backward_kernel<true, 4>) : go(balance_backward_kernel<true, 8>);
+  return E <= 128 ? go(balance_backward_kernel<false, 4>) : go(balance_backward_kernel<false, 8>);
 }
 
 cudaError_t launch_gate_backward(const uint16_t* dout, const float* yw, const int32_t* topk_idx,
