@@ -491,10 +491,11 @@ __global__ void __launch_bounds__(kGateThreads) gate_backward_kernel(
 
 // ------------------------------------------- router gradient, few tokens ----
 // One launch on the CUDA cores for batches whose three outputs take less time
-// than the tensor-core path's four launches. Every block computes 8 rows by 256
+// than the tensor-core path's three launches. Every block computes 8 rows by 128
 // columns of a product out[r][i] = sum_k A[k][r] B[k][i]: dW (r experts, k
-// tokens, B = x) or dx (r tokens, k experts, B = W); four groups of 64 threads
-// take every fourth k, a thread four columns.
+// tokens, B = x) or dx (r tokens, k experts, B = W). Its eight warps take every
+// eighth k, eight of them with their loads in flight together (four groups with
+// one load after another took 0.1 us a token), a lane four columns.
 
 // Four columns of an input row: x, or q 2^(s - 127) r g.
 struct RouterRows {
@@ -504,8 +505,9 @@ struct RouterRows {
   const float* rstd;
   const float* g;
 };
+template <bool Q8>
 __device__ __forceinline__ float4 router_row4(const RouterRows& r, int64_t t, int i, int d) {
-  if (r.x) {
+  if (!Q8) {
     const uint2 v = __ldg(reinterpret_cast<const uint2*>(r.x + t * d + i));
     return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
                        __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
@@ -531,35 +533,38 @@ struct SmallArgs {
   int* status;
 };
 
-constexpr int kChunk = 64;   // k staged at a time
+constexpr int kChunk = 64;    // k staged at a time, eight per warp
 
+template <bool Q8>
 __global__ void __launch_bounds__(256) router_small_kernel(const SmallArgs a) {
   pdl_wait_and_trigger();
   __shared__ float4 A[kChunk][2];          // eight rows of A
   __shared__ uint8_t keep[kChunk];
-  __shared__ float4 part[3][8][64];
-  const int tid = threadIdx.x, grp = tid >> 6, c = tid & 63;
+  __shared__ float4 part[4][8][32];        // sums of half of the warps
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int blk = blockIdx.x;
   if (blk == 0 && tid == 0) *a.status = 0;
   if (blk >= a.dw_blocks + a.dx_blocks) {
     // db: 32 experts, eight warps over the tokens
     __shared__ float sums[8][32];
-    const int e = (blk - a.dw_blocks - a.dx_blocks) * 32 + (tid & 31), w = tid >> 5;
+    const int e = (blk - a.dw_blocks - a.dx_blocks) * 32 + lane;
     float s = 0.f;
-    if (e < a.E)
-      for (int t = w; t < a.T; t += 8)
-        if (!a.mask || a.mask[t] != 0) s += __ldg(a.dl + static_cast<int64_t>(t) * a.E + e);
-    sums[w][tid & 31] = s;
+    if (e < a.E) {
+#pragma unroll 8
+      for (int t = warp; t < a.T; t += 8)
+        if (!a.mask || __ldg(a.mask + t) != 0) s += __ldg(a.dl + static_cast<int64_t>(t) * a.E + e);
+    }
+    sums[warp][lane] = s;
     __syncthreads();
-    if (w == 0 && e < a.E) {
-      for (int k = 1; k < 8; ++k) s += sums[k][tid & 31];
+    if (warp == 0 && e < a.E) {
+      for (int k = 1; k < 8; ++k) s += sums[k][lane];
       a.db[e] = a.accumulate ? a.db[e] + s : s;
     }
     return;
   }
   const bool is_dw = blk < a.dw_blocks;
   if (!is_dw) blk -= a.dw_blocks;
-  const int i = (blk % a.col_blocks) * 256 + c * 4, r0 = blk / a.col_blocks * 8;
+  const int i = (blk % a.col_blocks) * 128 + lane * 4, r0 = blk / a.col_blocks * 8;
   const int K = is_dw ? a.T : a.E, R = is_dw ? a.E : a.T;
   float* Af = reinterpret_cast<float*>(A);
   float4 acc[8];
@@ -567,79 +572,74 @@ __global__ void __launch_bounds__(256) router_small_kernel(const SmallArgs a) {
   for (int r = 0; r < 8; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k0 = 0; k0 < K; k0 += kChunk) {
     const int n = K - k0 < kChunk ? K - k0 : kChunk;
+    // this warp's rows of B, loaded whether or not their tokens are live
+    float4 b[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int kk = warp + 8 * u;
+      b[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (kk < n && i < a.d)
+        b[u] = is_dw ? router_row4<Q8>(a.rows, k0 + kk, i, a.d)
+                     : __ldg(reinterpret_cast<const float4*>(a.W + static_cast<int64_t>(k0 + kk) * a.d + i));
+    }
     __syncthreads();
     for (int v = tid; v < kChunk * 8; v += 256) {
       const int kk = is_dw ? v >> 3 : v & (kChunk - 1), r = is_dw ? v & 7 : v / kChunk;
       const int64_t t = is_dw ? k0 + kk : r0 + r;
       const int e = is_dw ? r0 + r : k0 + kk;
-      const bool live = t < a.T && (!a.mask || a.mask[t] != 0);
+      const bool live = t < a.T && (!a.mask || __ldg(a.mask + t) != 0);
       Af[kk * 8 + r] = live && e < a.E ? __ldg(a.dl + t * a.E + e) : 0.f;
       if (r == 0) keep[kk] = is_dw ? live : kk < n;
     }
     __syncthreads();
-    if (i < a.d) {
-#pragma unroll 4
-      for (int kk = grp; kk < n; kk += 4) {
-        if (!keep[kk]) continue;   // a padded token's row is not read
-        const float4 b = is_dw ? router_row4(a.rows, k0 + kk, i, a.d)
-                               : __ldg(reinterpret_cast<const float4*>(
-                                     a.W + static_cast<int64_t>(k0 + kk) * a.d + i));
-        const float4 lo = A[kk][0], hi = A[kk][1];
-        const float w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          acc[r].x = fmaf(w[r], b.x, acc[r].x);
-          acc[r].y = fmaf(w[r], b.y, acc[r].y);
-          acc[r].z = fmaf(w[r], b.z, acc[r].z);
-          acc[r].w = fmaf(w[r], b.w, acc[r].w);
-        }
+    for (int u = 0; u < 8; ++u) {
+      const int kk = warp + 8 * u;
+      if (!keep[kk]) continue;   // a padded token's row may hold anything
+      const float4 lo = A[kk][0], hi = A[kk][1];
+      const float w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        acc[r].x = fmaf(w[r], b[u].x, acc[r].x);
+        acc[r].y = fmaf(w[r], b[u].y, acc[r].y);
+        acc[r].z = fmaf(w[r], b[u].z, acc[r].z);
+        acc[r].w = fmaf(w[r], b[u].w, acc[r].w);
       }
     }
   }
-  if (grp > 0)
+  // warps 4..7 hand their sums to 0..3, those to warp r (row r) in order
+  auto add = [](float4 x, float4 y) { return make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w); };
+  if (warp >= 4)
 #pragma unroll
-    for (int r = 0; r < 8; ++r) part[grp - 1][r][c] = acc[r];
+    for (int r = 0; r < 8; ++r) part[warp - 4][r][lane] = acc[r];
   __syncthreads();
-  // group q finishes rows q and q + 4
-  if (grp == 0)
+  if (warp < 4)
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const float4 x = part[0][r][c], y = part[1][r][c], z = part[2][r][c];
-      part[0][r][c] = make_float4(acc[r].x + x.x + (y.x + z.x), acc[r].y + x.y + (y.y + z.y),
-                                  acc[r].z + x.z + (y.z + z.z), acc[r].w + x.w + (y.w + z.w));
-    }
+    for (int r = 0; r < 8; ++r) part[warp][r][lane] = add(acc[r], part[warp][r][lane]);
   __syncthreads();
-  if (i >= a.d) return;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = grp + 4 * h;
-    if (r0 + r >= R) continue;
-    float4 s = part[0][r][c];
-    const int64_t at = static_cast<int64_t>(r0 + r) * a.d + i;
-    if (is_dw) {
-      float4* o = reinterpret_cast<float4*>(a.dW + at);
-      if (a.accumulate) {
-        const float4 b = *o;
-        s = make_float4(s.x + b.x, s.y + b.y, s.z + b.z, s.w + b.w);
-      }
-      *o = s;
-    } else {
-      if (a.dx_in) {
-        const uint2 v = *reinterpret_cast<const uint2*>(a.dx_in + at);
-        s.x += __uint_as_float(v.x << 16);
-        s.y += __uint_as_float(v.x & 0xFFFF0000u);
-        s.z += __uint_as_float(v.y << 16);
-        s.w += __uint_as_float(v.y & 0xFFFF0000u);
-      }
-      const __nv_bfloat162 p = __floats2bfloat162_rn(s.x, s.y), q = __floats2bfloat162_rn(s.z, s.w);
-      *reinterpret_cast<uint2*>(a.dx + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&p),
-                                                        *reinterpret_cast<const uint32_t*>(&q));
+  if (i >= a.d || r0 + warp >= R) return;
+  float4 s = add(add(part[0][warp][lane], part[1][warp][lane]), add(part[2][warp][lane], part[3][warp][lane]));
+  const int64_t at = static_cast<int64_t>(r0 + warp) * a.d + i;
+  if (is_dw) {
+    float4* o = reinterpret_cast<float4*>(a.dW + at);
+    *o = a.accumulate ? add(s, *o) : s;
+  } else {
+    if (a.dx_in) {
+      const uint2 v = *reinterpret_cast<const uint2*>(a.dx_in + at);
+      s = add(s, make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
+                             __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u)));
     }
+    const __nv_bfloat162 p = __floats2bfloat162_rn(s.x, s.y), q = __floats2bfloat162_rn(s.z, s.w);
+    *reinterpret_cast<uint2*>(a.dx + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&p),
+                                                      *reinterpret_cast<const uint32_t*>(&q));
   }
 }
 
-// Most tokens of the one-launch path.
-constexpr int kSmallTokens = 128;
+// Which path. Measured, one launch against the tensor cores (d = 2880 unless said):
+// E = 32: T = 128 8.7 against 10.5 us, T = 192 11.6 against 10.7; E = 4, d = 512:
+// T = 128 7.3 against 9.0, T = 192 10.4 against 9.4; E = 128: T = 64 11.5 against
+// 17, T = 128 19.6 against 17.7.
+bool few_tokens(int E, int T, int d) { return T <= (static_cast<int64_t>(E) * d > 1 << 18 ? 96 : 144); }
 
 }  // namespace
 
@@ -702,11 +702,11 @@ cudaError_t launch_gate_backward(const uint16_t* dout, const float* yw, const in
 }
 
 size_t router_grad_scratch_bytes(int E, int T, int d) {
-  return T <= kSmallTokens ? 16 : router_grad_tc_scratch_bytes(E, T, d);
+  return few_tokens(E, T, d) ? 16 : router_grad_tc_scratch_bytes(E, T, d);
 }
 
 cudaError_t launch_router_backward(const RouterGradProblem& p, cudaStream_t st) {
-  if (p.T > kSmallTokens) return launch_router_backward_tc(p, st);
+  if (!few_tokens(p.E, p.T, p.d)) return launch_router_backward_tc(p, st);
   SmallArgs a;
   a.dl = p.dlogits;
   a.W = p.W_r;
@@ -715,7 +715,7 @@ cudaError_t launch_router_backward(const RouterGradProblem& p, cudaStream_t st) 
   a.E = p.E;
   a.T = p.T;
   a.d = p.d;
-  a.col_blocks = (p.d + 255) / 256;
+  a.col_blocks = (p.d + 127) / 128;
   a.dw_blocks = p.dW ? (p.E + 7) / 8 * a.col_blocks : 0;
   a.dx_blocks = p.dx ? (p.T + 7) / 8 * a.col_blocks : 0;
   a.accumulate = p.accumulate;
@@ -726,7 +726,8 @@ cudaError_t launch_router_backward(const RouterGradProblem& p, cudaStream_t st) 
   a.status = p.status;
   const int blocks = a.dw_blocks + a.dx_blocks + (p.db ? (p.E + 31) / 32 : 0);
   if (blocks == 0) return cudaSuccess;
-  return launch_kernel(router_small_kernel, dim3(blocks), dim3(256), 0, st, a);
+  return p.q ? launch_kernel(router_small_kernel<true>, dim3(blocks), dim3(256), 0, st, a)
+             : launch_kernel(router_small_kernel<false>, dim3(blocks), dim3(256), 0, st, a);
 }
 
 }  // namespace moe

@@ -1070,6 +1070,7 @@ cudaError_t launch_router_backward_tc(const RouterGradProblem& g, cudaStream_t s
   sums.accumulate = g.accumulate;
   sums.dW = g.dW;
   sums.db = g.db;
+  const size_t items = g.dW ? static_cast<size_t>(g.E) * g.d / 4 : static_cast<size_t>(g.E) * 32;
   if (g.dx) {
     DxArgs a;
     a.W = g.W_r;
@@ -1079,9 +1080,12 @@ cudaError_t launch_router_backward_tc(const RouterGradProblem& g, cudaStream_t s
     a.p = p;
     // the widest tile whose part of W leaves room for four boxes and four units
     a.n_tile = p.ep <= 96 ? 256 : p.ep <= 128 ? 192 : p.ep <= 192 ? 128 : 64;
+    // few token tiles: narrow ones, so that W's conversion is spread over the SMs
+    // (T = 512, E = 128, d = 2880: 17 us against 21; T = 2048: 26 against 23)
+    const int ttiles = (g.T + kTM - 1) / kTM;
+    if (ttiles <= 8) a.n_tile = 64;
     a.full = g.d / a.n_tile;
     const int part = (g.d - a.full * a.n_tile + 63) / 64, per = a.n_tile / 64;
-    const int ttiles = (g.T + kTM - 1) / kTM;
     // CTAs in proportion to the columns, one per SM where d allows
     a.splits = a.full ? kPlanSms * per / (a.full * per + part) : 0;
     if (a.splits > ttiles) a.splits = ttiles;
@@ -1124,12 +1128,14 @@ cudaError_t launch_router_backward_tc(const RouterGradProblem& g, cudaStream_t s
     if ((e = allow_smem(router_dx_kernel, done)) != cudaSuccess) return e;
     const int blocks = a.full * a.splits + a.last_splits;
     a.sums = sums;
-    a.sums.blocks = g.dW || g.db ? blocks : 0;
-    return launch_kernel(router_dx_kernel, dim3(blocks), dim3(kDxThreads),
+    // the sums are warps 12..15's where the tiles outlast them, else a launch of their own
+    const bool apart = ttiles <= 16 && items > static_cast<size_t>(blocks) * 32 * kSumsWarps * 3;
+    a.sums.blocks = (g.dW || g.db) && !apart ? blocks : 0;
+    e = launch_kernel(router_dx_kernel, dim3(blocks), dim3(kDxThreads),
                       static_cast<size_t>(a.off_fixed) + kFixed + 1024, st, tmD, tmIn, tmOut, a);
+    if (e != cudaSuccess || a.sums.blocks) return e;
   }
   if (!g.dW && !g.db) return cudaSuccess;
-  const size_t items = g.dW ? static_cast<size_t>(g.E) * g.d / 4 : static_cast<size_t>(g.E) * 32;
   const size_t want = (items + 255) / 256;
   sums.blocks = static_cast<int>(want < kPlanSms * 8 ? want : kPlanSms * 8);
   return launch_kernel(router_sums_kernel, dim3(sums.blocks), dim3(256), 0, st, sums);
