@@ -583,7 +583,7 @@ MOE_API moe_status moe_gate_backward(const void* dout_dev, const float* yw_dev,
  * or all four NULL).
  * dW_dev [E][d] f32, db_dev [E] f32, dx_dev [T][d] bf16: each may be NULL (not
  * computed; without dW no rows are read). dx_in_dev [T][d] bf16 or NULL, may
- * be dx_dev itself; accumulate concerns dW and db. A padded token's dx row is
+ * be dx_dev itself (no other output may overlap an input); accumulate concerns dW and db. A padded token's dx row is
  * its dx_in row (0 without one).
  * dW and db: fp32 products and sums (above 96 to 144 tokens on the tensor cores,
  * dlogits in three bf16 terms: nothing of its 24 bits is lost above 2^-110). dx:

@@ -7,7 +7,7 @@
 // r_t moves to the other operand (ds r_t, one fp32 rounding) and g_i to the sum.
 // The fp32 operands are split into bf16 terms hi, mid, lo, each the rounding of
 // what the ones before leave:
-//   dW  three terms of ds (24 bits: nothing is lost above 2^-126). The tensor
+//   dW  three terms of ds (24 bits: nothing is lost above 2^-110). The tensor
 //       core's accumulator loses up to an fp32 step per addition (a sum over
 //       1365 tokens was off by 1.6e-6 of its norm, one over 512 by 6e-7), so
 //       every kFlush tokens the sums move to registers and start anew
@@ -658,6 +658,7 @@ struct DxArgs {
   int off_ring, off_staging, off_fixed;
   int tmem_cols;
   bool has_in;
+  bool after_dw;                      // the launch before is the dW kernel, not the terms'
   SumArgs sums;
   int* status;
 };
@@ -780,9 +781,12 @@ __global__ void __launch_bounds__(kDxThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // W alone was read before the wait: this launch follows one of its own pass,
-  // which began after everything before the pass, W's writer included, had ended
-  pdl_wait_and_trigger();
+  // W alone was read so far, and the terms are all that most of the block reads
+  // from here. Behind the dW kernel only warps 12..15 wait, for that kernel's parts:
+  // this grid was launched once each of its blocks had passed its own wait, so the
+  // terms are complete and everything before the pass, W's writer included, has
+  // ended; tiles of dx are computed wherever an SM is free of dW's.
+  if (!a.after_dw || warp >= 4 + kOutWarps) pdl_wait_and_trigger();
   const uint32_t tmem = misc[0];
 
   if (warp == 0) {
@@ -1113,6 +1117,7 @@ cudaError_t launch_router_backward_tc(const RouterGradProblem& g, cudaStream_t s
     a.off_fixed = a.off_staging + a.staging * kUnitBytes;
     a.tmem_cols = tmem_columns(2 * a.n_tile);
     a.has_in = g.dx_in != nullptr;
+    a.after_dw = g.dW != nullptr;
     a.status = g.status;
     CUtensorMap tmD, tmIn = {}, tmOut;
     {
