@@ -199,18 +199,23 @@ __global__ void __launch_bounds__(256) router_terms_kernel(const float* __restri
     // [token][4] 16-bit words, bit 8 set for a padded token and past the last one
     const int G = d / 32;
     const int64_t end = blockIdx.x + 1 == gridDim.x ? padded_tokens(T) : t1;
-    const int64_t items = (end - t0) * p.tiles_d;
-    for (int64_t v = threadIdx.x; v < items; v += 256) {
-      const int tile = static_cast<int>(v % p.tiles_d);
-      const int64_t t = t0 + v / p.tiles_d;
-      const bool row = t < T;
-      const uint32_t dead = !row || (mask && mask[t] == 0) ? 0x100u : 0u;
-      uint32_t w[4];
+    uint2* const to = reinterpret_cast<uint2*>(words) + t0;
+    const int64_t pitch = padded_tokens(T);
+    // neighbouring threads: neighbouring tiles of a token (the scales' order)
+    for (int64_t b0 = t0; b0 < end; b0 += 1024) {
+      const int items = static_cast<int>(end - b0 < 1024 ? end - b0 : 1024) * p.tiles_d;
+#pragma unroll 4
+      for (int v = threadIdx.x; v < items; v += 256) {
+        const int i = v / p.tiles_d, tile = v - i * p.tiles_d;
+        const int64_t t = b0 + i;
+        const bool row = t < T;
+        const uint8_t* const from = scales + t * G + tile * 4;
+        const uint32_t dead = !row || (mask && __ldg(mask + t) == 0) ? 0x100u : 0u;
+        uint32_t w[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[k] = dead | (row && tile * 4 + k < G ? __ldg(scales + t * G + tile * 4 + k) : 127u);
-      reinterpret_cast<uint2*>(words)[tile * static_cast<int64_t>(padded_tokens(T)) + t] =
-          make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+        for (int k = 0; k < 4; ++k) w[k] = dead | (row && tile * 4 + k < G ? __ldg(from + k) : 127u);
+        to[tile * pitch + (t - t0)] = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+      }
     }
   }
   sum[threadIdx.x] = make_float2(sa, sb);
