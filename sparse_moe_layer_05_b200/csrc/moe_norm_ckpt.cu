@@ -339,11 +339,13 @@ NormBwdShape norm_bwd_shape(int T, int d) {
   const int vec = d / 8;                         // at most 2048
   s.chunks = vec <= kNormThreads ? 1 : vec <= 2 * kNormThreads ? 2 : 4;
   s.threads = ((vec + s.chunks - 1) / s.chunks + 31) / 32 * 32;
-  // blocks that fill an SM's threads about half, at most three where rows are long
-  // (each leaves a row of partial sums: at d = 2880 three leave 5 MB, beside 165 MB
-  // of rows at T = 8192) and sixteen where they are short
+  // blocks of about 1152 threads per SM, at most eight: at d = 2880 three (two or
+  // four took 50 us where three took 43, T = 8192). Each leaves a row of partial sums
+  // to the launch after: at d = 96, T = 4096 sixteen took 10.7 us, eight 8.3; at
+  // T = 16384 14.8 and 15.3, four 21.8. (Joining the rows of a cluster first was no
+  // faster: its blocks have to find room together.)
   int per = 1152 / s.threads;
-  per = per < 1 ? 1 : per > 16 ? 16 : per;
+  per = per < 1 ? 1 : per > 8 ? 8 : per;
   s.blocks = T < 148 * per ? (T > 0 ? T : 1) : 148 * per;
   return s;
 }
