@@ -342,6 +342,19 @@ def test_router_gradients(T, E, d, rows):
     assert all(torch.equal(o3[n].view(torch.int16), o[n].view(torch.int16)) for n in o)
 
 
+# every layout of the terms (experts rounded up to 16: 16 .. 128 in one group, two
+# groups above), each side of the paths' borders, one 64-column tile and part tiles
+LAYOUTS = [(1000, 3, 32), (144, 60, 64), (145, 60, 64), (96, 200, 2880), (97, 200, 2880), (145, 256, 64),
+           (1500, 100, 320), (700, 90, 448), (2600, 80, 96), (900, 161, 128), (5000, 200, 64), (1100, 112, 2080),
+           (1030, 17, 8256)]
+
+
+@pytest.mark.parametrize("rows", ["bf16", "8bit"])
+@pytest.mark.parametrize("T,E,d", LAYOUTS)
+def test_router_gradients_of_every_layout(T, E, d, rows):
+    test_router_gradients(T, E, d, rows)
+
+
 @pytest.mark.parametrize("want", [("dW",), ("db",), ("dx",), ("dW", "db"), ("db", "dx")])
 @pytest.mark.parametrize("T,E,d", [(33, 16, 96), (3000, 40, 256)])
 def test_router_gradients_by_themselves(T, E, d, want):
