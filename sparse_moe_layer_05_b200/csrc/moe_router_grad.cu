@@ -644,7 +644,10 @@ bool few_tokens(int E, int T, int d) { return T <= (static_cast<int64_t>(E) * d 
 }  // namespace
 
 size_t balance_scratch_bytes(int E, int T) {
-  return static_cast<size_t>(kBalClusters) * 12 + static_cast<size_t>(balance_clusters(T)) * E * 8;
+  // a row for every cluster there may be: one more token per warp can take fewer
+  // clusters, and a workspace for more tokens serves fewer too
+  const int rows = T <= kBalOneCluster ? 1 : kBalClusters;
+  return static_cast<size_t>(kBalClusters) * 12 + static_cast<size_t>(rows) * E * 8;
 }
 
 cudaError_t launch_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask,

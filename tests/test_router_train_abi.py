@@ -120,3 +120,15 @@ def test_workspace_sizes():
     assert B.moe_router_backward_workspace_size(4, 8, 40) == 0
     assert B.moe_rms_norm_backward_workspace_size(8, 16416) == 0
     assert B.moe_rms_norm_backward_workspace_size(-1, 64) == 0
+
+
+def test_a_workspace_for_more_tokens_serves_fewer(lib):
+    """Sizes never fall as T grows: a caller sizes a workspace for its largest batch."""
+    Ts = [*range(0, 700), *range(700, 40000, 131)]
+    sizes = {f"balance {E}": [lib.moe_balance_loss_workspace_size(E, 1, T) for T in Ts] for E in (1, 32, 256)}
+    sizes |= {f"router {E} {d}": [lib.moe_router_backward_workspace_size(E, T, d) for T in Ts]
+              for E, d in ((4, 512), (32, 2880), (161, 64), (248, 2880))}
+    sizes |= {f"norm {d}": [lib.moe_rms_norm_backward_workspace_size(T, d) for T in Ts] for d in (32, 2880, 16384)}
+    for name, s in sizes.items():
+        falls = [Ts[i] for i in range(1, len(s)) if s[i] < s[i - 1]]
+        assert not falls, (name, falls[:3])
