@@ -624,8 +624,15 @@ __global__ void __launch_bounds__(256) router_small_kernel(const SmallArgs a) {
     float4* o = reinterpret_cast<float4*>(a.dW + at);
     *o = a.accumulate ? add(s, *o) : s;
   } else {
+    // a padded token's row stays dx_in's (its sum may be zero times an infinity)
+    const bool live = !a.mask || __ldg(a.mask + r0 + warp) != 0;
+    if (!live) s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (a.dx_in) {
       const uint2 v = *reinterpret_cast<const uint2*>(a.dx_in + at);
+      if (!live) {
+        *reinterpret_cast<uint2*>(a.dx + at) = v;
+        return;
+      }
       s = add(s, make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
                              __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u)));
     }

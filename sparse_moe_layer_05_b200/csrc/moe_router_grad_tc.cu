@@ -655,6 +655,7 @@ constexpr int kMaxRing = 8, kMaxStaging = 8;
 
 struct DxArgs {
   const float* W;
+  const uint8_t* mask;
   int E, T, d;
   Plan p;
   int n_tile;                         // columns per tile
@@ -886,6 +887,9 @@ __global__ void __launch_bounds__(kDxThreads, 1)
     int waited = -1;
     for (int q = half; q < n * units; q += 2) {
       const int j = q / units, u = q % units, b = j & 1, s = q % a.staging;
+      // a padded token's row stays dx_in's (its sum may be zero times an infinity)
+      const int64_t t = static_cast<int64_t>(tile_row(j)) + r;
+      const bool live = !a.mask || t >= a.T || __ldg(a.mask + t) != 0;
       for (; waited < j; ++waited)
         if ((units > 1 || ((waited + 1) & 1) == half) &&
             !warp_wait(bar_acc((waited + 1) & 1), (waited + 1) >> 1 & 1, abort_flag, a.status))
@@ -915,13 +919,14 @@ __global__ void __launch_bounds__(kDxThreads, 1)
             w[2] = x.z;
             w[3] = x.w;
           }
+          if (live)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const __nv_bfloat162 z = __floats2bfloat162_rn(
-                __uint_as_float(v[8 * h + 2 * k]) + __uint_as_float(w[k] << 16),
-                __uint_as_float(v[8 * h + 2 * k + 1]) + __uint_as_float(w[k] & 0xFFFF0000u));
-            w[k] = *reinterpret_cast<const uint32_t*>(&z);
-          }
+            for (int k = 0; k < 4; ++k) {
+              const __nv_bfloat162 z = __floats2bfloat162_rn(
+                  __uint_as_float(v[8 * h + 2 * k]) + __uint_as_float(w[k] << 16),
+                  __uint_as_float(v[8 * h + 2 * k + 1]) + __uint_as_float(w[k] & 0xFFFF0000u));
+              w[k] = *reinterpret_cast<const uint32_t*>(&z);
+            }
           *o = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
@@ -1083,6 +1088,7 @@ cudaError_t launch_router_backward_tc(const RouterGradProblem& g, cudaStream_t s
   if (g.dx) {
     DxArgs a;
     a.W = g.W_r;
+    a.mask = g.mask;
     a.E = g.E;
     a.T = g.T;
     a.d = g.d;

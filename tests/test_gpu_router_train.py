@@ -369,6 +369,23 @@ def test_router_gradients_by_themselves(T, E, d, want):
         assert torch.equal(some[n].view(torch.int16), every[n].view(torch.int16)), n
 
 
+@pytest.mark.parametrize("T,E,d", [(1, 3, 32), (60, 20, 96), (700, 20, 96), (2700, 40, 320), (1500, 200, 64)])
+@pytest.mark.parametrize("with_in", [False, True])
+def test_a_padded_tokens_dx_stays_under_weights_that_are_no_numbers(T, E, d, with_in):
+    """dx of a padded token is its dx_in row, bit for bit, or 0, whatever the weights
+    hold; a live token's shows the infinity."""
+    rng = np.random.default_rng(T)
+    dl, Wr = rng.standard_normal((T, E)).astype(np.float32), rng.standard_normal((E, d)).astype(np.float32)
+    Wr[0, 5], Wr[E - 1, 9] = np.inf, np.nan
+    live = rng.random(T) < 0.7
+    live[-1] = T > 1 and T % 2 == 0
+    dx_in = bits(np.where(rng.random((T, d)) < 0.2, -0.0, rng.standard_normal((T, d)))) if with_in else None
+    o = run_router(dl, Wr, {}, live.astype(np.uint8), dx_in, want=("dx",))["dx"].cpu().numpy()
+    assert np.array_equal(o[~live], dx_in[~live] if with_in else 0 * o[~live])
+    v = val(o[live])
+    assert not np.isfinite(v[:, [5, 9]]).any() and np.isfinite(np.delete(v, [5, 9], 1)).all()
+
+
 def test_router_gradients_of_values_at_the_types_ends():
     """Gradients near fp32's smallest normal numbers, weights and rows near bf16's
     largest; a zero batch. Terms below 2^-126 are lost: at most 2^-126 each."""
