@@ -735,7 +735,7 @@ cudaError_t launch_router_backward(const RouterGradProblem& p, cudaStream_t st) 
   a.dx = p.dx;
   a.status = p.status;
   const int blocks = a.dw_blocks + a.dx_blocks + (p.db ? (p.E + 31) / 32 : 0);
-  if (blocks == 0) return cudaSuccess;
+  if (blocks == 0) return cudaMemsetAsync(p.status, 0, sizeof(int), st);   // dx of no tokens
   return p.q ? launch_kernel(router_small_kernel<true>, dim3(blocks), dim3(256), 0, st, a)
              : launch_kernel(router_small_kernel<false>, dim3(blocks), dim3(256), 0, st, a);
 }

@@ -559,6 +559,16 @@ def test_no_tokens():
     guarded()
 
 
+def test_no_tokens_leave_a_status():
+    from sparse_moe_layer_05_b200 import binding as B
+    E, d = 6, 64
+    z = lambda *s, dtype=torch.float32: torch.zeros(*s, dtype=dtype, device="cuda")
+    ws = ws_of(B.moe_router_backward_workspace_size(E, 0, d)).fill_(9)
+    B.moe_router_backward(z(0, E), z(E, d), E, 0, d, None, None, z(0, d, dtype=torch.bfloat16), ws)
+    torch.cuda.synchronize()
+    assert not ws[:4].any()
+
+
 def test_tensors_of_another_size_type_or_place_are_refused():
     from sparse_moe_layer_05_b200 import binding as B
     T, E, k, d = 8, 4, 2, 64
