@@ -883,13 +883,18 @@ __global__ void __launch_bounds__(kDxThreads, 1)
   } else if (warp >= 4 && warp < 4 + kOutWarps) {
     const int quad = warp & 3, half = (warp - 4) >> 2, r = quad * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    // the mask's byte of the lane's token in unit q, loaded a unit ahead
+    auto live_byte = [&](int q) -> uint32_t {
+      const int64_t t = static_cast<int64_t>(tile_row(q / units)) + r;
+      return a.mask && q < n * units && t < a.T ? __ldg(a.mask + t) : 1u;
+    };
+    uint32_t next_live = live_byte(half);
     // this group's units, counted over all tiles: half, half + 2, ...
     int waited = -1;
     for (int q = half; q < n * units; q += 2) {
       const int j = q / units, u = q % units, b = j & 1, s = q % a.staging;
-      // a padded token's row stays dx_in's (its sum may be zero times an infinity)
-      const int64_t t = static_cast<int64_t>(tile_row(j)) + r;
-      const bool live = !a.mask || t >= a.T || __ldg(a.mask + t) != 0;
+      const bool live = next_live != 0;
+      next_live = live_byte(q + 2);
       for (; waited < j; ++waited)
         if ((units > 1 || ((waited + 1) & 1) == half) &&
             !warp_wait(bar_acc((waited + 1) & 1), (waited + 1) >> 1 & 1, abort_flag, a.status))
@@ -919,15 +924,18 @@ __global__ void __launch_bounds__(kDxThreads, 1)
             w[2] = x.z;
             w[3] = x.w;
           }
-          if (live)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const __nv_bfloat162 z = __floats2bfloat162_rn(
-                  __uint_as_float(v[8 * h + 2 * k]) + __uint_as_float(w[k] << 16),
-                  __uint_as_float(v[8 * h + 2 * k + 1]) + __uint_as_float(w[k] & 0xFFFF0000u));
-              w[k] = *reinterpret_cast<const uint32_t*>(&z);
-            }
-          *o = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int k = 0; k < 4; ++k) {
+            const __nv_bfloat162 z = __floats2bfloat162_rn(
+                __uint_as_float(v[8 * h + 2 * k]) + __uint_as_float(w[k] << 16),
+                __uint_as_float(v[8 * h + 2 * k + 1]) + __uint_as_float(w[k] & 0xFFFF0000u));
+            w[k] = *reinterpret_cast<const uint32_t*>(&z);
+          }
+          // a padded token's row stays dx_in's (its sum may be zero times an infinity)
+          if (live)
+            *o = make_uint4(w[0], w[1], w[2], w[3]);
+          else if (!a.has_in)
+            *o = make_uint4(0, 0, 0, 0);
         }
       }
       fence_proxy_async_smem();
