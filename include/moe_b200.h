@@ -512,8 +512,8 @@ MOE_API int moe_forward_launch_count(int E, int k, int T, int d, int I);
  *   streams with workspaces of their own may run at the same time, and each may
  *   be captured into a CUDA graph.
  * - A NaN or an infinity in a live token's inputs shows as NaN (or infinity) in
- *   the outputs that depend on it; a logits' gradient beyond bf16's largest value
- *   (3.39e38) counts as an infinity in moe_router_backward.
+ *   the outputs that depend on it; a logits' gradient or a weight beyond bf16's
+ *   largest value (3.39e38) may count as an infinity in moe_router_backward.
  * - Every sum over tokens has a fixed order: the same call gives the same bits.
  */
 
@@ -583,8 +583,9 @@ MOE_API moe_status moe_gate_backward(const void* dout_dev, const float* yw_dev,
  * or all four NULL).
  * dW_dev [E][d] f32, db_dev [E] f32, dx_dev [T][d] bf16: each may be NULL (not
  * computed; without dW no rows are read). dx_in_dev [T][d] bf16 or NULL, may
- * be dx_dev itself (no other output may overlap an input); accumulate concerns dW and db. A padded token's dx row is
- * its dx_in row (0 without one).
+ * be dx_dev itself (no other output may overlap an input); accumulate concerns
+ * dW and db. A padded token's dx row is its dx_in row (0 without one), whatever
+ * W_r holds.
  * dW and db: fp32 products and sums (above 96 to 144 tokens on the tensor cores,
  * dlogits in three bf16 terms: nothing of its 24 bits is lost above 2^-110). dx:
  * there dlogits and W_r in two bf16 terms, off by at most 2^-16 of
@@ -607,6 +608,10 @@ MOE_API moe_status moe_router_backward(const float* dlogits_dev, const float* W_
  *   q_dev [T][d] E4M3, scales_dev [T][d/32] E8M0: h as moe_mx_quantize with
  *         MOE_ACT_MXFP8 converts it, byte for byte
  *   rstd_dev [T] f32: 1 / sqrt(mean(h_t^2) + eps)
+ * A NaN in a row makes its rstd NaN, and with it all that is computed from the
+ * checkpoint. Where the sum of squares is infinite in fp32 (an infinity in h, or
+ * values above 1.8e19) rstd is 0 and x moe_rms_norm's, q holds the largest code for
+ * an infinity, and the row counts as zeros to the backward pass.
  */
 MOE_API moe_status moe_rms_norm_checkpoint(const void* h_dev, const float* g_dev, float eps, int T,
                                            int d, void* x_dev, uint8_t* q_dev,
@@ -633,7 +638,8 @@ MOE_API moe_status moe_rms_norm_backward(const void* dx_dev, const void* h_dev,
 /*
  * moe_forward_block whose norm also leaves the checkpoint (q_dev, scales_dev,
  * rstd_dev as moe_rms_norm_checkpoint): the training form of the sublayer.
- * Same arguments, output bits, errors and launches otherwise; the logits,
+ * Same arguments, output bits, errors and launches otherwise (no array may be
+ * NULL, T = 0 or not, as there); the logits,
  * choices, weights and weighted rows that the backward pass reads stay in the
  * workspace (moe_workspace_layout) until its next use.
  */
