@@ -715,6 +715,7 @@ constexpr int kSumsWarps = 4;
 constexpr int kUnitBytes = kTM * 128;
 constexpr int kDxThreads = 128 + 32 * (kOutWarps + kSumsWarps);
 
+template <bool MASKED>
 __global__ void __launch_bounds__(kDxThreads, 1)
     router_dx_kernel(const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmIn,
                      const __grid_constant__ CUtensorMap tmOut, const DxArgs a) {
@@ -900,7 +901,7 @@ __global__ void __launch_bounds__(kDxThreads, 1)
     // the mask's byte of the lane's token in unit q, loaded a unit ahead
     auto live_byte = [&](int q) -> uint32_t {
       const int64_t t = static_cast<int64_t>(tile_row(q / units)) + r;
-      return a.mask && q < n * units && t < a.T ? __ldg(a.mask + t) : 1u;
+      return MASKED && q < n * units && t < a.T ? __ldg(a.mask + t) : 1u;
     };
     uint32_t next_live = live_byte(half);
     // this group's units, counted over all tiles: half, half + 2, ...
@@ -946,7 +947,7 @@ __global__ void __launch_bounds__(kDxThreads, 1)
             w[k] = *reinterpret_cast<const uint32_t*>(&z);
           }
           // a padded token's row stays dx_in's (its sum may be zero times an infinity)
-          if (live)
+          if (!MASKED || live)
             *o = make_uint4(w[0], w[1], w[2], w[3]);
           else if (!a.has_in)
             *o = make_uint4(0, 0, 0, 0);
@@ -1162,15 +1163,20 @@ cudaError_t launch_router_backward_tc(const RouterGradProblem& g, cudaStream_t s
       if (a.has_in && !mx_encode_bf16_map(&tmIn, g.dx_in, 2, dims, strides, box))
         return cudaErrorInvalidValue;
     }
-    static bool done[64] = {false};
-    if ((e = allow_smem(router_dx_kernel, done)) != cudaSuccess) return e;
+    static bool done[2][64] = {{false}};
     const int blocks = a.full * a.splits + a.last_splits;
     a.sums = sums;
     // the sums are warps 12..15's where the tiles outlast them, else a launch of their own
     const bool apart = ttiles <= 16 && items > static_cast<size_t>(blocks) * 32 * kSumsWarps * 3;
     a.sums.blocks = (g.dW || g.db) && !apart ? blocks : 0;
-    e = launch_kernel(router_dx_kernel, dim3(blocks), dim3(kDxThreads),
-                      static_cast<size_t>(a.off_fixed) + kFixed + 1024, st, tmD, tmIn, tmOut, a);
+    auto go = [&](auto kernel, bool (&set)[64]) {
+      const cudaError_t err = allow_smem(kernel, set);
+      return err != cudaSuccess ? err
+                                : launch_kernel(kernel, dim3(blocks), dim3(kDxThreads),
+                                                static_cast<size_t>(a.off_fixed) + kFixed + 1024, st, tmD,
+                                                tmIn, tmOut, a);
+    };
+    e = g.mask ? go(router_dx_kernel<true>, done[0]) : go(router_dx_kernel<false>, done[1]);
     if (e != cudaSuccess || a.sums.blocks) return e;
   }
   if (!g.dW && !g.db) return cudaSuccess;
