@@ -20,8 +20,10 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 // serialization may start while its predecessor on the stream is still
 // running; griddepcontrol.wait blocks until that predecessor has completed and
 // its memory is visible (a no-op for kernels launched without it). Every
-// kernel of the library executes it before its first global-memory access, so
-// by induction all earlier kernels of the stream have completed by then. The
+// kernel of the library executes it, in every thread and under no condition,
+// before its first global-memory access (router_dx_kernel: before its first access
+// to anything that a kernel of the pass writes), so by induction all earlier
+// kernels of the stream have completed by then. The
 // trigger lets the stream's next kernel be scheduled once every CTA of this
 // one has started (its CTAs then wait in griddepcontrol.wait).
 __device__ __forceinline__ void pdl_wait_and_trigger() {

@@ -678,7 +678,6 @@ struct DxArgs {
   int off_ring, off_staging, off_fixed;
   int tmem_cols;
   bool has_in;
-  bool after_dw;                      // the launch before is the dW kernel, not the terms'
   SumArgs sums;
   int* status;
 };
@@ -802,12 +801,13 @@ __global__ void __launch_bounds__(kDxThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // W alone was read so far, and the terms are all that most of the block reads
-  // from here. Behind the dW kernel only warps 12..15 wait, for that kernel's parts:
-  // this grid was launched once each of its blocks had passed its own wait, so the
-  // terms are complete and everything before the pass, W's writer included, has
-  // ended; tiles of dx are computed wherever an SM is free of dW's.
-  if (!a.after_dw || warp >= 4 + kOutWarps) pdl_wait_and_trigger();
+  // W alone was read so far: it is no kernel's of this pass, and whatever wrote it
+  // ended before the pass's first kernel began. All else waits for the launch before,
+  // behind which dW's parts and the terms are complete. (Tiles begun without the wait,
+  // on the grounds that the dW kernel's blocks had waited for the terms, were 4 us
+  // earlier at T = 192, E = 248 and no earlier from T = 8192 on; but memory written by
+  // earlier grids is visible only to a grid that waits itself.)
+  pdl_wait_and_trigger();
   const uint32_t tmem = misc[0];
 
   if (warp == 0) {
@@ -1151,7 +1151,6 @@ cudaError_t launch_router_backward_tc(const RouterGradProblem& g, cudaStream_t s
     a.off_fixed = a.off_staging + a.staging * kUnitBytes;
     a.tmem_cols = tmem_columns(2 * a.n_tile);
     a.has_in = g.dx_in != nullptr;
-    a.after_dw = g.dW != nullptr;
     a.status = g.status;
     CUtensorMap tmD, tmIn = {}, tmOut;
     {
