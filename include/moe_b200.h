@@ -587,9 +587,13 @@ MOE_API moe_status moe_gate_backward(const void* dout_dev, const float* yw_dev,
  * dW and db. A padded token's dx row is its dx_in row (0 without one), whatever
  * W_r holds.
  * dW and db: fp32 products and sums (above 96 to 144 tokens on the tensor cores,
- * dlogits in three bf16 terms: nothing of its 24 bits is lost above 2^-110). dx:
- * there dlogits and W_r in two bf16 terms, off by at most 2^-16 of
- * sum_e |dlogits W_r| before its rounding to bf16.
+ * dlogits in three bf16 terms: nothing of its 24 bits is lost above 2^-110; of 8-bit
+ * rows that holds for the product dlogits rstd, which is rounded to fp32 first).
+ * dx: below that an fp32 product; on the tensor cores dlogits and W_r enter as two
+ * fp16 terms, 22 bits. Before its rounding to bf16 it is off by at most
+ * (2^-20 + 3 E 2^-27) sum_e |dlogits W_r|, the second part for the additions, plus
+ * what values far below their neighbours lose: of a token's dlogits 2^-39 of the
+ * largest (or 2^-151) times |W_r|, of W_r as much of its largest times |dlogits|.
  */
 MOE_API size_t moe_router_backward_workspace_size(int E, int T, int d);
 MOE_API moe_status moe_router_backward(const float* dlogits_dev, const float* W_r_dev,

@@ -371,6 +371,15 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// kind::f16 with fp16 A and B: the same instruction, its types are the descriptor's.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  umma_bf16(d_tmem, adesc, bdesc, idesc, accumulate);
+}
+
 // ------------------------------------------- block-scaled (MX) tcgen05 ----
 
 // D[tmem] (+)= sum_k (a_mk 2^(sa_m - 127)) (b_nk 2^(sb_n - 127)) over one

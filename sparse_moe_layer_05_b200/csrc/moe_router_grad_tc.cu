@@ -1,19 +1,24 @@
 // moe_router_grad_tc.cu -- gradients of the router product s = x W^T + b:
 //   dW = ds^T x,  db = sum_t ds,  dx = bf16(ds W + dx_in)
-// on the tensor cores (kind::f16, bf16 operands, fp32 accumulators).
+// on the tensor cores (kind::f16, fp32 accumulators).
 //
 // Precision. x is bf16, or an 8-bit checkpoint row q 2^(s-127) r_t g_i whose
 // q 2^(s-127) has four significant bits: both enter an UMMA exactly, the row's
 // r_t moves to the other operand (ds r_t, one fp32 rounding) and g_i to the sum.
-// The fp32 operands are split into bf16 terms hi, mid, lo, each the rounding of
-// what the ones before leave:
-//   dW  three terms of ds (24 bits: nothing is lost above 2^-110). The tensor
+// The fp32 operands are split into terms hi, mid, lo, each the rounding of what the
+// ones before leave:
+//   dW  three bf16 terms of ds (24 bits: nothing is lost above 2^-110). The tensor
 //       core's accumulator loses up to an fp32 step per addition (a sum over
 //       1365 tokens was off by 1.6e-6 of its norm, one over 512 by 6e-7), so
 //       every kFlush tokens the sums move to registers and start anew
-//   dx  two terms of ds and of W, products hi hi, mid hi and hi mid: off by at
-//       most 3 2^-18 of each product, 2^-7 of what the bf16 output's own
-//       rounding leaves
+//   dx  two fp16 terms of ds and of W (22 bits), products mid hi, hi mid and hi hi:
+//       off by at most 3 2^-22 of each product. fp16's range is brought over each
+//       token's gradients and over the weights of a tile of columns by powers of
+//       two, which leave with the output's rounding; below 2^-29 of the largest of
+//       those a value keeps fewer bits, 2^-39 of the largest being lost at most.
+//       (Two bf16 terms, 16 bits, cost the same and changed the rounded output by
+//       1.3e-4 of its norm where the order of an fp32 sum changes it by 3e-5, E = 128;
+//       three would double the products.)
 // A padded token's terms are zero, and its row of x is zeroed in shared memory
 // (it may hold a NaN).
 //
@@ -21,6 +26,7 @@
 // dW's parts. No operand is transposed in memory: tokens are K of the first product
 // (both operands MN-major) and M of the second (ds K-major, W MN-major).
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 #include "moe_internal.h"
@@ -49,7 +55,7 @@ struct Plan {
   int lo;          // first column of the lo terms (hi at 0, mid at egp)
   int panels;      // panels of a group's three terms
   int ep;          // E rounded up to 16
-  int dx_panel;    // first panel of the two terms the dx product reads
+  int dx_panel;    // first panel of the terms the dx product reads: mid, then hi
   int all;         // panels in all
   int bt;          // tokens per stage of the dW kernel
   int tiles_d, splits, term_blocks;
@@ -66,11 +72,8 @@ Plan make_plan(int E, int T, int d, bool scaled, int num_sms) {
   p.lo = p.accs == 3 ? 2 * p.egp : (2 * p.egp + 63) / 64 * 64;
   p.panels = (p.lo + p.egp + 63) / 64;
   p.ep = (E + 15) / 16 * 16;
-  // one group's hi and mid terms lie next to each other and serve both products,
-  // unless dW's are those of ds r
-  const bool shared = p.groups == 1 && !scaled;
-  p.dx_panel = shared ? 0 : p.groups * p.panels;
-  p.all = p.groups * p.panels + (shared ? 0 : (2 * p.ep + 63) / 64);
+  p.dx_panel = p.groups * p.panels;
+  p.all = p.dx_panel + (2 * p.ep + 63) / 64;
   // at least four stages fit; 8-bit rows need room as codes too
   p.bt = p.panels <= (scaled ? 3 : 5) ? 64 : 32;
   p.tiles_d = (d + kMD - 1) / kMD;
@@ -101,95 +104,154 @@ __device__ __forceinline__ Terms split3(float v) {
   return t;
 }
 
+struct HalfTerms {
+  __half hi, mid;
+};
+__device__ __forceinline__ HalfTerms split2h(float v) {
+  HalfTerms t;
+  t.hi = __float2half_rn(v);
+  t.mid = __float2half_rn(v - __half2float(t.hi));
+  return t;
+}
+__device__ __forceinline__ uint32_t pack2(__half a, __half b) {
+  return __half_as_ushort(a) | (static_cast<uint32_t>(__half_as_ushort(b)) << 16);
+}
+// |v|, or 0 for what is no finite number: infinities and NaNs set no scale.
+__device__ __forceinline__ float finite_size(float v) {
+  const float a = fabsf(v);
+  return a < __int_as_float(0x7F800000) ? a : 0.f;
+}
+__device__ __forceinline__ float exp2_int(int k) { return __int_as_float((k + 127) << 23); }   // -126 .. 127
+// k that brings 2^k times the largest value into [2^14, 2^15), fp16's upper end, as
+// far as 2^k is a normal fp32 number with a normal inverse: -113 .. 126.
+__device__ __forceinline__ int half_scale(float largest) {
+  const int k = 141 - static_cast<int>(__float_as_uint(largest) >> 23);
+  return k > 126 ? 126 : k;
+}
+
 // Tokens of a tile's scale words: a stage's words are one aligned piece.
 __host__ __device__ constexpr int64_t padded_tokens(int T) { return (static_cast<int64_t>(T) + 63) / 64 * 64; }
 
 // Rows [t0, t1) of the terms per block; a thread holds one pair of experts, so
-// its sum for db stays in registers. Blocks sum consecutive tokens.
+// its sum for db stays in registers. Blocks sum consecutive tokens. The `lanes`
+// threads of a row join its largest value over shuffles, above 64 experts over
+// shared memory too.
 constexpr int kTermRows = 4;          // rows a thread loads at a time
 
 __global__ void __launch_bounds__(256) router_terms_kernel(const float* __restrict__ dl,
                                                            const float* __restrict__ rstd,
                                                            const uint8_t* __restrict__ scales,
                                                            const uint8_t* __restrict__ mask, int E,
-                                                           int T, int d, const Plan p, int lanes,
+                                                           int T, int d, const Plan p, int lanes, bool dw,
                                                            uint16_t* __restrict__ terms,
                                                            uint16_t* __restrict__ words,
+                                                           int8_t* __restrict__ exps,
                                                            float* __restrict__ db_part, int* status) {
   pdl_wait_and_trigger();
   if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
   __shared__ float2 sum[256];
+  __shared__ uint32_t tops[2][kTermRows][8];   // a warp's largest values, two rounds in turn
   const int64_t t0 = static_cast<int64_t>(T) * blockIdx.x / gridDim.x;
   const int64_t t1 = static_cast<int64_t>(T) * (blockIdx.x + 1) / gridDim.x;
   const int pair = threadIdx.x % lanes, row = threadIdx.x / lanes, rows = 256 / lanes;
-  const int e = 2 * pair;
-  const bool even = (E & 1) == 0;
+  const int e = 2 * pair, warp = threadIdx.x >> 5;
+  const bool even = (E & 1) == 0, stores = e < p.ep;
   const size_t panel = static_cast<size_t>(T) * 64;
   // address of column c for token 0
   auto column = [&](int first, int c) { return terms + (first + (c >> 6)) * panel + (c & 63); };
   float sa = 0.f, sb = 0.f;
-  if (e < p.ep) {
-    const bool together = p.groups == 1;
-    // the pair's places among dW's columns (a group may start at an odd expert)
-    const int ga = e / p.eg, gb = (e + 1) / p.eg, ca = e - ga * p.eg, cb = e + 1 - gb * p.eg;
-    uint16_t* const hi_a = column(together ? 0 : ga * p.panels, together ? e : ca);
-    uint16_t* const mid_a = column(together ? 0 : ga * p.panels, p.egp + (together ? e : ca));
-    uint16_t* const lo_a = column(together ? 0 : ga * p.panels, p.lo + (together ? e : ca));
-    uint16_t* const hi_b = column(gb * p.panels, cb);
-    uint16_t* const mid_b = column(gb * p.panels, p.egp + cb);
-    uint16_t* const lo_b = column(gb * p.panels, p.lo + cb);
-    uint16_t* const hi_x = column(p.dx_panel, e);
-    uint16_t* const mid_x = column(p.dx_panel, p.ep + e);
-    for (int64_t base = t0 + row; base < t1; base += rows * kTermRows) {
-      float a[kTermRows], b[kTermRows], r[kTermRows];
+  const bool together = p.groups == 1;
+  // the pair's places among dW's columns (a group may start at an odd expert)
+  const int ga = e / p.eg, gb = (e + 1) / p.eg, ca = e - ga * p.eg, cb = e + 1 - gb * p.eg;
+  uint16_t* const hi_a = column(together ? 0 : ga * p.panels, together ? e : ca);
+  uint16_t* const mid_a = column(together ? 0 : ga * p.panels, p.egp + (together ? e : ca));
+  uint16_t* const lo_a = column(together ? 0 : ga * p.panels, p.lo + (together ? e : ca));
+  uint16_t* const hi_b = column(gb * p.panels, cb);
+  uint16_t* const mid_b = column(gb * p.panels, p.egp + cb);
+  uint16_t* const lo_b = column(gb * p.panels, p.lo + cb);
+  uint16_t* const mid_x = column(p.dx_panel, e);
+  uint16_t* const hi_x = column(p.dx_panel, p.ep + e);
+  int round = 0;
+  for (int64_t base = t0; base < t1; base += rows * kTermRows, round ^= 1) {   // the block as one
+    float a[kTermRows], b[kTermRows], r[kTermRows];
 #pragma unroll
-      for (int k = 0; k < kTermRows; ++k) {
-        const int64_t t = base + k * rows;
-        a[k] = b[k] = 0.f;
-        r[k] = 1.f;
-        if (t < t1 && e < E && (mask == nullptr || mask[t] != 0)) {
-          if (even) {
-            const float2 v = __ldg(reinterpret_cast<const float2*>(dl + t * E + e));
-            a[k] = v.x;
-            b[k] = v.y;
-          } else {
-            a[k] = __ldg(dl + t * E + e);
-            if (e + 1 < E) b[k] = __ldg(dl + t * E + e + 1);
-          }
-          if (rstd) r[k] = __ldg(rstd + t);
+    for (int k = 0; k < kTermRows; ++k) {
+      const int64_t t = base + row + k * rows;
+      a[k] = b[k] = 0.f;
+      r[k] = 1.f;
+      if (t < t1 && e < E && (mask == nullptr || mask[t] != 0)) {
+        if (even) {
+          const float2 v = __ldg(reinterpret_cast<const float2*>(dl + t * E + e));
+          a[k] = v.x;
+          b[k] = v.y;
+        } else {
+          a[k] = __ldg(dl + t * E + e);
+          if (e + 1 < E) b[k] = __ldg(dl + t * E + e + 1);
         }
+        if (rstd) r[k] = __ldg(rstd + t);
+      }
+    }
+    if (exps) {
+      // sizes compare as their bits do
+      uint32_t top[kTermRows];
+#pragma unroll
+      for (int k = 0; k < kTermRows; ++k)
+        top[k] = __float_as_uint(fmaxf(finite_size(a[k]), finite_size(b[k])));
+      if (lanes < 32) {
+        for (int off = lanes >> 1; off > 0; off >>= 1)
+#pragma unroll
+          for (int k = 0; k < kTermRows; ++k) top[k] = max(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], off));
+      } else {
+#pragma unroll
+        for (int k = 0; k < kTermRows; ++k) top[k] = __reduce_max_sync(0xFFFFFFFFu, top[k]);
+      }
+      if (lanes > 32) {
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+          for (int k = 0; k < kTermRows; ++k) tops[round][k][warp] = top[k];
+        __syncthreads();
+        const int first = warp & ~((lanes >> 5) - 1);
+        for (int w = first; w < first + (lanes >> 5); ++w)
+#pragma unroll
+          for (int k = 0; k < kTermRows; ++k) top[k] = max(top[k], tops[round][k][w]);
       }
 #pragma unroll
       for (int k = 0; k < kTermRows; ++k) {
-        const int64_t t = base + k * rows;
-        if (t >= t1) continue;
+        const int64_t t = base + row + k * rows;
+        if (t >= t1 || !stores) continue;
+        const int ex = half_scale(__uint_as_float(top[k]));
+        const float up = exp2_int(ex);
+        const HalfTerms u = split2h(a[k] * up), v = split2h(b[k] * up);
         const size_t at = static_cast<size_t>(t) * 64;
-        sa += a[k];
-        sb += b[k];
-        Terms u = split3(a[k]), v = split3(b[k]);
-        if (p.dx_panel) {
-          *reinterpret_cast<uint32_t*>(hi_x + at) = pack2(u.hi, v.hi);
-          *reinterpret_cast<uint32_t*>(mid_x + at) = pack2(u.mid, v.mid);
-          if (rstd) {
-            u = split3(a[k] * r[k]);
-            v = split3(b[k] * r[k]);
-          }
+        *reinterpret_cast<uint32_t*>(mid_x + at) = pack2(u.mid, v.mid);
+        *reinterpret_cast<uint32_t*>(hi_x + at) = pack2(u.hi, v.hi);
+        if (pair == 0) exps[t] = static_cast<int8_t>(ex);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kTermRows; ++k) {
+      const int64_t t = base + row + k * rows;
+      if (t >= t1) continue;
+      sa += a[k];
+      sb += b[k];
+      if (!dw || !stores) continue;
+      const size_t at = static_cast<size_t>(t) * 64;
+      // r is 1 where the rows are bf16
+      const Terms u = split3(a[k] * r[k]), v = split3(b[k] * r[k]);
+      if (together) {
+        *reinterpret_cast<uint32_t*>(hi_a + at) = pack2(u.hi, v.hi);
+        *reinterpret_cast<uint32_t*>(mid_a + at) = pack2(u.mid, v.mid);
+        *reinterpret_cast<uint32_t*>(lo_a + at) = pack2(u.lo, v.lo);
+      } else {
+        if (e < E) {
+          hi_a[at] = __bfloat16_as_ushort(u.hi);
+          mid_a[at] = __bfloat16_as_ushort(u.mid);
+          lo_a[at] = __bfloat16_as_ushort(u.lo);
         }
-        if (together) {
-          *reinterpret_cast<uint32_t*>(hi_a + at) = pack2(u.hi, v.hi);
-          *reinterpret_cast<uint32_t*>(mid_a + at) = pack2(u.mid, v.mid);
-          *reinterpret_cast<uint32_t*>(lo_a + at) = pack2(u.lo, v.lo);
-        } else {
-          if (e < E) {
-            hi_a[at] = __bfloat16_as_ushort(u.hi);
-            mid_a[at] = __bfloat16_as_ushort(u.mid);
-            lo_a[at] = __bfloat16_as_ushort(u.lo);
-          }
-          if (e + 1 < E) {
-            hi_b[at] = __bfloat16_as_ushort(v.hi);
-            mid_b[at] = __bfloat16_as_ushort(v.mid);
-            lo_b[at] = __bfloat16_as_ushort(v.lo);
-          }
+        if (e + 1 < E) {
+          hi_b[at] = __bfloat16_as_ushort(v.hi);
+          mid_b[at] = __bfloat16_as_ushort(v.mid);
+          lo_b[at] = __bfloat16_as_ushort(v.lo);
         }
       }
     }
@@ -670,6 +732,7 @@ constexpr int kMaxRing = 8, kMaxStaging = 8;
 struct DxArgs {
   const float* W;
   const uint8_t* mask;
+  const int8_t* exps;                 // [T]: a token's terms are 2^exps[t] ds
   int E, T, d;
   Plan p;
   int n_tile;                         // columns per tile
@@ -713,6 +776,11 @@ constexpr int kOutWarps = 8;
 constexpr int kSumsWarps = 4;
 constexpr int kUnitBytes = kTM * 128;
 constexpr int kDxThreads = 128 + 32 * (kOutWarps + kSumsWarps);
+// eight weights at a time: a thread's share of a tile, at most 384 experts times
+// 64-column units (launch_router_backward_tc's choice of n_tile)
+constexpr int kDxWeights = 384;
+constexpr int kDxChunks = kDxWeights * 8 / kDxThreads;
+constexpr int kDxTops = 8;            // misc words of the warps' largest weights
 
 template <bool MASKED>
 __global__ void __launch_bounds__(kDxThreads, 1)
@@ -773,22 +841,42 @@ __global__ void __launch_bounds__(kDxThreads, 1)
     tmem_alloc(smem_u32(misc), static_cast<uint32_t>(a.tmem_cols));
     tmem_relinquish();
   }
-  // W's columns i0 .. i0 + cols - 1 as hi rows 0 .. ep - 1, mid rows ep .. 2 ep - 1
+  // W's columns i0 .. i0 + cols - 1 times 2^kw as hi rows 0 .. ep - 1, mid rows
+  // ep .. 2 ep - 1
   const int chunks = cols / 8;
-#pragma unroll 3
-  for (int v = threadIdx.x; v < a.p.ep * chunks; v += kDxThreads) {
-    const int e = v / chunks, ch = v % chunks, i = i0 + ch * 8;
-    float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  float w[kDxChunks][8], top = 0.f;
+#pragma unroll
+  for (int n = 0; n < kDxChunks; ++n) {
+    const int v = threadIdx.x + n * kDxThreads;
+    const int e = v / chunks, i = i0 + v % chunks * 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[n][j] = 0.f;
     if (e < a.E && i < a.d) {
       const float4 x = __ldg(reinterpret_cast<const float4*>(a.W + static_cast<size_t>(e) * a.d + i));
       const float4 y = __ldg(reinterpret_cast<const float4*>(a.W + static_cast<size_t>(e) * a.d + i) + 1);
-      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-      w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+      w[n][0] = x.x; w[n][1] = x.y; w[n][2] = x.z; w[n][3] = x.w;
+      w[n][4] = y.x; w[n][5] = y.y; w[n][6] = y.z; w[n][7] = y.w;
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_size(w[n][j]));
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+  if (lane == 0) misc[kDxTops + warp] = __float_as_uint(top);
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kDxThreads / 32; ++k) top = fmaxf(top, __uint_as_float(misc[kDxTops + k]));
+  const int kw = half_scale(top);
+  const float up = exp2_int(kw);
+#pragma unroll
+  for (int n = 0; n < kDxChunks; ++n) {
+    const int v = threadIdx.x + n * kDxThreads;
+    const int e = v / chunks, ch = v % chunks;
+    if (e >= a.p.ep) continue;
     uint32_t hi[4], mid[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const Terms p = split3(w[2 * j]), q = split3(w[2 * j + 1]);
+      const HalfTerms p = split2h(w[n][2 * j] * up), q = split2h(w[n][2 * j + 1] * up);
       hi[j] = pack2(p.hi, q.hi);
       mid[j] = pack2(p.mid, q.mid);
     }
@@ -827,7 +915,7 @@ __global__ void __launch_bounds__(kDxThreads, 1)
       }
     if (lane == 0) misc[2] = static_cast<uint32_t>(issued);
   } else if (warp == 1) {
-    const uint32_t idesc = idesc_bf16_f32(kTM, cols) | kBMnMajor;
+    const uint32_t idesc = idesc_f16_f32(kTM, cols) | kBMnMajor;
     const int steps = a.p.ep / 16;                     // K steps of a term
     const uint64_t a0 = sdesc_k_sw128(sbase + a.off_ring), w0 = sdesc_mn_sw128(sbase, wblock);
     int s = 0, ph = 0, consumed = 0;
@@ -837,7 +925,7 @@ __global__ void __launch_bounds__(kDxThreads, 1)
       if (!(ok = warp_wait(bar_free(b), ((j >> 1) & 1) ^ 1, abort_flag, a.status))) break;
       tc_fence_after();
       const uint32_t acc = tmem + b * a.n_tile;
-      int step = 0;                                    // ds's hi steps, then its mid steps
+      int step = 0;      // ds's mid steps, then its hi steps: small products come first
       for (int x = 0; x < a.boxes; ++x) {
         if (!(ok = warp_wait(bar_full(s), ph, abort_flag, a.status))) break;
         ++consumed;
@@ -848,10 +936,10 @@ __global__ void __launch_bounds__(kDxThreads, 1)
           for (int kk = 0; kk < 4; ++kk) {
             const int st = step + kk;
             if (st >= 2 * steps) break;
-            const bool mid = st >= steps;
-            const uint64_t wd = advance(w0, static_cast<uint32_t>(mid ? st - steps : st) * 2048);
-            umma_bf16(acc, advance(ad, kk * 32), wd, idesc, st != 0);
-            if (!mid) umma_bf16(acc, advance(ad, kk * 32), advance(wd, wblock / 2), idesc, 1u);
+            const bool mid = st < steps;
+            const uint64_t wd = advance(w0, static_cast<uint32_t>(mid ? st : st - steps) * 2048);
+            if (!mid) umma_f16(acc, advance(ad, kk * 32), advance(wd, wblock / 2), idesc, 1u);
+            umma_f16(acc, advance(ad, kk * 32), wd, idesc, st != 0);
           }
           umma_commit(bar_empty(s));
           if (x + 1 == a.boxes) umma_commit(bar_acc(b));
@@ -898,18 +986,25 @@ __global__ void __launch_bounds__(kDxThreads, 1)
   } else if (warp >= 4 && warp < 4 + kOutWarps) {
     const int quad = warp & 3, half = (warp - 4) >> 2, r = quad * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    // the mask's byte of the lane's token in unit q, loaded a unit ahead
-    auto live_byte = [&](int q) -> uint32_t {
+    // the exponent and the mask's byte of the lane's token in unit q, loaded a unit ahead
+    uint32_t next_live = 1;
+    int next_k = 0;
+    auto load_token = [&](int q) {
       const int64_t t = static_cast<int64_t>(tile_row(q / units)) + r;
-      return MASKED && q < n * units && t < a.T ? __ldg(a.mask + t) : 1u;
+      if (q >= n * units || t >= a.T) return;
+      next_k = __ldg(a.exps + t);
+      if (MASKED) next_live = __ldg(a.mask + t);
     };
-    uint32_t next_live = live_byte(half);
+    load_token(half);
     // this group's units, counted over all tiles: half, half + 2, ...
     int waited = -1;
     for (int q = half; q < n * units; q += 2) {
       const int j = q / units, u = q % units, b = j & 1, s = q % a.staging;
       const bool live = next_live != 0;
-      next_live = live_byte(q + 2);
+      // 2^-(the terms' exponents) as two factors: one alone may pass fp32's range
+      const int k = -(next_k + kw);
+      const float f0 = exp2_int(k >> 1), f1 = exp2_int(k - (k >> 1));
+      load_token(q + 2);
       for (; waited < j; ++waited)
         if ((units > 1 || ((waited + 1) & 1) == half) &&
             !warp_wait(bar_acc((waited + 1) & 1), (waited + 1) >> 1 & 1, abort_flag, a.status))
@@ -942,8 +1037,8 @@ __global__ void __launch_bounds__(kDxThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const __nv_bfloat162 z = __floats2bfloat162_rn(
-                __uint_as_float(v[8 * h + 2 * k]) + __uint_as_float(w[k] << 16),
-                __uint_as_float(v[8 * h + 2 * k + 1]) + __uint_as_float(w[k] & 0xFFFF0000u));
+                fmaf(__uint_as_float(v[8 * h + 2 * k]) * f0, f1, __uint_as_float(w[k] << 16)),
+                fmaf(__uint_as_float(v[8 * h + 2 * k + 1]) * f0, f1, __uint_as_float(w[k] & 0xFFFF0000u)));
             w[k] = *reinterpret_cast<const uint32_t*>(&z);
           }
           // a padded token's row stays dx_in's (its sum may be zero times an infinity)
@@ -987,6 +1082,7 @@ int tmem_columns(int need) {
 struct Scratch {
   uint16_t* terms;
   uint16_t* words;
+  int8_t* exps;
   float* db_part;
   float* part;
   size_t bytes;
@@ -1003,10 +1099,12 @@ Scratch scratch_of(void* base, const Plan& p, int E, int T, int d) {
   };
   const size_t terms = take(static_cast<size_t>(T) * p.all * 128);
   const size_t words = take(static_cast<size_t>(padded_tokens(T)) * p.tiles_d * 8);
+  const size_t exps = take(static_cast<size_t>(T));
   const size_t db = take(static_cast<size_t>(p.term_blocks) * E * 4);
   const size_t part = take(static_cast<size_t>(p.splits) * E * d * 4);
   s.terms = reinterpret_cast<uint16_t*>(b + terms);
   s.words = reinterpret_cast<uint16_t*>(b + words);
+  s.exps = reinterpret_cast<int8_t*>(b + exps);
   s.db_part = reinterpret_cast<float*>(b + db);
   s.part = reinterpret_cast<float*>(b + part);
   s.bytes = off;
@@ -1039,8 +1137,9 @@ cudaError_t launch_router_backward_tc(const RouterGradProblem& g, cudaStream_t s
   int lanes = 8;
   while (2 * lanes < p.ep) lanes *= 2;
   cudaError_t e = launch_kernel(router_terms_kernel, dim3(p.term_blocks), dim3(256), 0, st, g.dlogits,
-                                q8 ? g.rstd : nullptr, g.scales, g.mask, g.E, g.T, g.d, p, lanes, sc.terms,
-                                q8 ? sc.words : nullptr, sc.db_part, g.status);
+                                q8 ? g.rstd : nullptr, g.scales, g.mask, g.E, g.T, g.d, p, lanes,
+                                g.dW != nullptr, sc.terms, q8 ? sc.words : nullptr,
+                                g.dx ? sc.exps : nullptr, sc.db_part, g.status);
   if (e != cudaSuccess) return e;
   pdl_launches() = true;
   auto encode_terms = [&](CUtensorMap* m, const cuuint32_t* box) {
@@ -1112,6 +1211,7 @@ cudaError_t launch_router_backward_tc(const RouterGradProblem& g, cudaStream_t s
     DxArgs a;
     a.W = g.W_r;
     a.mask = g.mask;
+    a.exps = sc.exps;
     a.E = g.E;
     a.T = g.T;
     a.d = g.d;
@@ -1136,6 +1236,7 @@ cudaError_t launch_router_backward_tc(const RouterGradProblem& g, cudaStream_t s
       if (a.last_splits > ttiles) a.last_splits = ttiles;
       if (a.last_splits < 1) a.last_splits = 1;
     }
+    if (p.ep * per > kDxWeights) return cudaErrorInvalidValue;   // no choice above gives this
     a.boxes = (2 * p.ep + 63) / 64;
     const int wbytes = p.ep * 256 * per;
     const int room = kSmemLimit - kFixed - wbytes;
