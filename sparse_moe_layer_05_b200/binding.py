@@ -607,6 +607,24 @@ def moe_selftest_wait_timeout(workspace, stream=None) -> None:
 
 # ----------------------------------------------------------- convenience ----
 
+def _result(T: int, d: int, device, stream):
+    """Room for a bf16 [T, d] result that kernels on `stream` (None: the current one)
+    write. The allocator hands a block out again in the order of the stream that it
+    was allocated on, so the block is `stream`'s; the current stream, where the caller
+    goes on with the tensor, is recorded with it."""
+    import torch
+    if stream is None:
+        return torch.empty((T, d), dtype=torch.uint16, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream), device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        out = torch.empty((T, d), dtype=torch.uint16, device=device)
+    if current != stream:
+        out.record_stream(current)
+    return out
+
+
 class NormCheckpoint:
     """What moe_forward_block_checkpoint leaves of its norm's input: E4M3 codes,
     E8M0 scales and the rows' inverse roots, for up to T tokens."""
@@ -667,12 +685,11 @@ class MoELayer:
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
 
     def forward(self, x, out=None, stream=None):
-        import torch
         T = x.shape[0]
         if T > self.T_max:
             raise ValueError("more tokens than the workspace was sized for")
         if out is None:
-            out = torch.empty((T, self.d), dtype=torch.uint16, device=x.device)
+            out = _result(T, self.d, x.device, stream)
         moe_forward(x, self.W_r, self.b_r, self.Wgu_codes, self.Wgu_scales, self.Wd_codes,
                     self.Wd_scales, self.E, self.k, T, self.d, self.I, out, self.workspace, stream)
         return out
@@ -681,12 +698,11 @@ class MoELayer:
                       stream=None):
         """out = h + MoE(RMSNorm(h)) (a layer made with block=True); with a
         checkpoint, the training form, whose backward pass is backward_block."""
-        import torch
         T = h.shape[0]
         if T > self.T_max:
             raise ValueError("more tokens than the workspace was sized for")
         if out is None:
-            out = torch.empty((T, self.d), dtype=torch.uint16, device=h.device)
+            out = _result(T, self.d, h.device, stream)
         args = (h, g, eps, self.W_r, self.b_r, self.Wgu_codes, self.Wgu_scales, self.Wd_codes,
                 self.Wd_scales, self.E, self.k, T, self.d, self.I, out)
         if checkpoint is None:
@@ -704,12 +720,11 @@ class MoELayer:
         balance_coef * balance + z_coef * z is weighted by dloss (f32 [1]; None: 1).
         The experts are frozen; their share of the gradient that reaches
         RMSNorm(h), if the caller has it, is dx_in bf16 [T, d]."""
-        import torch
         T = dout.shape[0]
         if T > grads.T:
             raise ValueError("more tokens than the gradients' buffers were sized for")
         if dh is None:
-            dh = torch.empty((T, self.d), dtype=torch.uint16, device=dout.device)
+            dh = _result(T, self.d, dout.device, stream)
         E, k, d, mask = self.E, self.k, self.d, token_mask
         logits, idx = self.intermediate("logits", T), self.intermediate("topk_idx", T)
         dlogits, dx, ws = grads.dlogits[:T], grads.dx[:T], grads.workspace
