@@ -28,4 +28,11 @@ __device__ __forceinline__ float e8m0_to_f32(uint32_t s) {
   return __uint_as_float(s == 0u ? 0x00400000u : s == 255u ? 0x7FC00000u : s << 23);
 }
 
+// The same for a checkpointed row whose inverse root is r: 0 where r is, so that the
+// row is zeros. A row that held an infinity has r = 0 and codes for 1.75 2^128, which
+// is fp32's infinity, and that times r would be a NaN.
+__device__ __forceinline__ float e8m0_of_row(uint32_t s, float r) {
+  return r == 0.f ? 0.f : e8m0_to_f32(s);
+}
+
 }  // namespace moe

@@ -243,7 +243,7 @@ __global__ void __maxnreg__(NC == 1 ? 56 : 128) norm_backward_kernel(
       }
       const uint32_t dw[4] = {next[c].dx.x, next[c].dx.y, next[c].dx.z, next[c].dx.w};
       if (Q8) {
-        const float2 s = both(e8m0_to_f32(next[c].scale));
+        const float2 s = both(e8m0_of_row(next[c].scale, r));
         const uint32_t hw[2] = {next[c].h.x, next[c].h.y};
 #pragma unroll
         for (int i = 0; i < 4; ++i)

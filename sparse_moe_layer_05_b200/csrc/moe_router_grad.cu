@@ -513,7 +513,7 @@ __device__ __forceinline__ float4 router_row4(const RouterRows& r, int64_t t, in
                        __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
   }
   const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(r.q + t * d + i));
-  const float s = e8m0_to_f32(__ldg(r.scales + t * (d / 32) + i / 32)), n = __ldg(r.rstd + t);
+  const float n = __ldg(r.rstd + t), s = e8m0_of_row(__ldg(r.scales + t * (d / 32) + i / 32), n);
   const float2 a = e4m3x2_to_f32x2(w & 0xFFFFu), b = e4m3x2_to_f32x2(w >> 16);
   const float4 g = __ldg(reinterpret_cast<const float4*>(r.g + i));
   return make_float4(a.x * s * n * g.x, a.y * s * n * g.y, b.x * s * n * g.z, b.y * s * n * g.w);

@@ -258,7 +258,9 @@ __global__ void __launch_bounds__(256) router_terms_kernel(const float* __restri
   }
   if (words) {
     // the 8-bit rows' scales as the dW kernel takes them: [tile of 128 columns]
-    // [token][4] 16-bit words, bit 8 set for a padded token and past the last one
+    // [token][4] 16-bit words, bit 8 set for rows that count as zeros: a padded token's,
+    // past the last one, and where the inverse root is 0 (the codes of an infinity are
+    // bf16's infinity, which the term's zero does not undo)
     const int G = d / 32;
     const int64_t end = blockIdx.x + 1 == gridDim.x ? padded_tokens(T) : t1;
     uint2* const to = reinterpret_cast<uint2*>(words) + t0;
@@ -272,7 +274,7 @@ __global__ void __launch_bounds__(256) router_terms_kernel(const float* __restri
         const int64_t t = b0 + i;
         const bool row = t < T;
         const uint8_t* const from = scales + t * G + tile * 4;
-        const uint32_t dead = !row || (mask && __ldg(mask + t) == 0) ? 0x100u : 0u;
+        const uint32_t dead = !row || __ldg(rstd + t) == 0.f || (mask && __ldg(mask + t) == 0) ? 0x100u : 0u;
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) w[k] = dead | (row && tile * 4 + k < G ? __ldg(from + k) : 127u);
@@ -629,7 +631,7 @@ __global__ void __launch_bounds__(128 + 32 * (kSumWarps + (Q8 ? kConvWarps : 0))
         const int row = 16 * u + tr;
         uint4 q = *reinterpret_cast<const uint4*>(codes + row * 128 + ((c ^ (row & 7)) << 4));
         uint32_t w = words[row * 4 + (c >> 1)];
-        if (w > 255u) {      // a padded token's row counts as zeros
+        if (w > 255u) {      // a row that counts as zeros
           q = make_uint4(0, 0, 0, 0);
           w = 127u;
         }
