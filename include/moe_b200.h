@@ -559,7 +559,9 @@ MOE_API moe_status moe_balance_loss_backward(const float* logits_dev, const floa
 /*
  * Gradient to the logits through the selected-set softmax and the weighted sum
  * out_t = sum_j p_j y_j: with A_j = <dout_t, p_j y_j> (fp32),
- *   dlogits[t, topk_idx_j] (+)= A_j - p_j sum_l A_l,   0 for the other experts.
+ *   dlogits[t, topk_idx_j] (+)= A_j - p_j sum_l A_l,   0 for the other experts,
+ * formed as sum_l (p_l A_j - p_j A_l), the same since a token's weights sum to 1: off
+ * by roundings of these products only, however close to 1 a weight is.
  *   dout_dev [T][d] bf16   gradient of the layer's output
  *   yw_dev   [T*k][d] f32  p-weighted expert rows in pair order t*k+j, as a
  *                          forward call leaves them (moe_workspace_layout's yw)

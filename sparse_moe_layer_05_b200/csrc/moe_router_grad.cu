@@ -9,6 +9,7 @@
 //
 //   out_t = sum_j p_j y_j over the selected set:  A_j = <dout_t, p_j y_j>,
 //   dL/ds[t, idx_j] = p_j (dp_j - sum_l p_l dp_l) = A_j - p_j sum_l A_l
+//                   = sum_l (p_l A_j - p_j A_l),  the p_l's sum being 1
 //
 //   s = x W^T + b:  dW = ds^T x,  db = sum_t ds,  dx = ds W
 //
@@ -466,13 +467,18 @@ __global__ void __launch_bounds__(kGateThreads) gate_backward_kernel(
   }
   __syncthreads();
   if (in && me < 32) {
-    // A_j over the token's warps, then its share of the sum over the slots
-    float a = 0.f;
+    // A_j over the token's warps, then the sum over pairs of slots. With p_j near 1,
+    // A_j - p_j sum A is a difference of near equals, and A_j (1 - sum p) with the
+    // weights' roundings comes on top: at 1 - p_j = 1e-5 it was off by 1e-2 of itself.
+    // A pair's two products are each rounded, so that a slot with itself gives zero.
+    float a = 0.f, p = 0.f, g = 0.f;
     const int first = tok * (span / 32);
     if (live && lane < k)
       for (int x = 0; x < span / 32; ++x) a += part[first + x][lane];
-    const float total = warp_sum(a);
-    grad[tok][lane] = live && lane < k ? a - __ldg(w + t * k + lane) * total : 0.f;
+    if (live && lane < k) p = __ldg(w + t * k + lane);
+    for (int l = 0; l < k; ++l)
+      g += __fmul_rn(__shfl_sync(0xFFFFFFFFu, p, l), a) - __fmul_rn(p, __shfl_sync(0xFFFFFFFFu, a, l));
+    grad[tok][lane] = live && lane < k ? g : 0.f;
     sidx[tok][lane] = live && lane < k ? __ldg(idx + t * k + lane) : -1;
   }
   __syncthreads();
