@@ -32,6 +32,16 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
   return v;
 }
+// Both sums at once: each half of the warp takes one of them (six shuffles, not ten).
+__device__ __forceinline__ void warp_sum2(float& a, float& b, int lane) {
+  const bool upper = lane & 16;
+  float v = (upper ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, upper ? a : b, 16);
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+  const float w = __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+  a = upper ? w : v;
+  b = upper ? v : w;
+}
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
@@ -366,10 +376,13 @@ __global__ void __launch_bounds__(256) balance_backward_kernel(
   for (; t < T; t += step) {
     const bool live = live_byte != 0 && l != -CUDART_INF_F;
     const float lt = l;
-    float p[NL], fp = 0.f;
+    // exp(s - lse) over its own sum: lse is fp32, off by up to 2^-24 |lse|, and every
+    // exponential of the row by that much of itself (3e-4 at logits of 1e4)
+    float p[NL], sum = 0.f, fp = 0.f;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       p[i] = live && expert_of<VEC>(lane, i) < E ? expf(v[i] - lt) : 0.f;
+      sum += p[i];
       fp = fmaf(f[i], p[i], fp);
     }
     if (t + step < T) {
@@ -377,11 +390,13 @@ __global__ void __launch_bounds__(256) balance_backward_kernel(
       if (mask) live_byte = __ldg(mask + t + step);
       load_row<VEC, NL>(logits + (t + step) * E, E, lane, v);
     }
-    fp = warp_sum(fp);
+    warp_sum2(fp, sum, lane);
     if (!live && accumulate) continue;   // left alone
+    const float norm = 1.f / sum, to = scale * norm;
+    fp *= norm;
     const float zt = 2.f * z_coef * lt;
 #pragma unroll
-    for (int i = 0; i < NL; ++i) p[i] = live ? scale * p[i] * (aE * (f[i] - fp) + zt) : 0.f;
+    for (int i = 0; i < NL; ++i) p[i] = live ? to * p[i] * (aE * (f[i] - fp) + zt) : 0.f;
     float* row = dlogits + t * E;
     if (VEC) {
 #pragma unroll
