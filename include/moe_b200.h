@@ -531,7 +531,9 @@ MOE_API int moe_forward_launch_count(int E, int k, int T, int d, int I);
  * An index outside 0..E-1 (a dropped pair, say -1) is not counted. A logit of
  * -inf has probability 0; a row of nothing but -inf adds nothing to P and z
  * (its lse is -inf) and gets no gradient. NaN and +inf in a live row give NaN.
- * Sums over tokens: T / 4096 + 32 terms at most in fp32, their sums in fp64.
+ * Sums over tokens: of p T / 4096 + 32 terms at most in fp32, their sums and those of
+ * lse^2 in fp64; balance and z enter the loss unrounded (a z beyond fp32's range is an
+ * infinity in stats, and no NaN in the loss where z_coef is 0).
  */
 MOE_API size_t moe_balance_loss_workspace_size(int E, int k, int T);
 MOE_API moe_status moe_balance_loss(const float* logits_dev, const int32_t* topk_idx_dev,

@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kBalWarps * 32) balance_partial_kernel(
   float acc[NL], next[NL];
 #pragma unroll
   for (int i = 0; i < NL; ++i) acc[i] = 0.f;
-  float z = 0.f;
+  double z = 0.0;                          // a square of lse may pass fp32's range
   int n = 0, next_idx = -1;
   uint32_t next_live = 1;
   const int64_t step = static_cast<int64_t>(gridDim.x) * warps;
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kBalWarps * 32) balance_partial_kernel(
     for (int i = 0; i < NL; ++i) acc[i] += v[i] * inv;
     if (lane == 0) {
       lse_out[t] = l;
-      if (!none) z = fmaf(l, l, z);
+      if (!none) z = fma(static_cast<double>(l), static_cast<double>(l), z);
     }
     if (static_cast<unsigned>(chosen) < static_cast<unsigned>(E)) atomicAdd(&bc[chosen], 1);
   }

@@ -39,3 +39,23 @@ def test_balance_gradient_of_an_offset(T, E, k, offset):
     # a row's gradients add up to nothing, but for roundings
     total = np.abs(f64(d).sum(1))
     assert (total <= 256 * U * size.sum(1) + 1e-38).all()
+
+
+@pytest.mark.parametrize("T", [40, 600])
+def test_z_loss_beyond_fp32s_range(T):
+    """lse = 1e20 in half of the rows: z is 5e39, an infinity in fp32; the loss holds the
+    balance term alone where its coefficient is 0, and 1e-30 z where it is that."""
+    E, k = 33, 2
+    rng = np.random.default_rng(T)
+    s = rng.standard_normal((T, E)).astype(np.float32)
+    idx = np.argsort(-s, axis=1)[:, :k].astype(np.int32)
+    s[::2] = -1e20
+    s[::2, 7] = 1e20
+    live = np.ones(T, bool)
+    for b in (0.0, 1e-30):
+        (loss, bal, z, n), *_ = R.balance_loss(s.astype(np.float64), idx, k, 1.0, float(np.float32(b)), live)
+        stats, *_, d = run_balance(s, idx, None, 1.0, b)
+        got = f64(stats)
+        assert np.isposinf(got[2]) and z > 1e39
+        close(got[:2], np.array([loss, bal]), 256 * U * np.array([abs(loss), bal]), "loss, balance")
+        assert np.isfinite(f64(d)).all()
