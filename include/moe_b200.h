@@ -484,17 +484,20 @@ MOE_API int moe_forward_launch_count(int E, int k, int T, int d, int I);
 
 /*
  * ------------------------------------------------------ training the router
- * The gradients a user needs to train the router (W_r, b_r) and the norm's
- * gain around frozen MXFP4 experts, next to the forward pass that leaves what
- * they read: moe_workspace_layout's logits, topk_idx, topk_w and yw, or
- * moe_route's outputs. Order of a backward pass for the sublayer
+ * The gradients a user needs to train the router (W_r, b_r) around frozen MXFP4
+ * experts, next to the forward pass that leaves what they read:
+ * moe_workspace_layout's logits, topk_idx, topk_w and yw, or moe_route's outputs;
+ * and the norm's, for what reaches it. Order of a backward pass for the sublayer
  * out = h + MoE(RMSNorm(h)), given dout [T][d]:
  *   moe_gate_backward           dlogits from dout and the weighted expert rows
  *   moe_balance_loss(_backward) the auxiliary loss, added to dlogits
  *   moe_router_backward         dW_r, db_r and dx = dlogits W_r (+ dx_in)
  *   moe_rms_norm_backward       dg and dh = dh_in + d/dh of the norm
- * The gradient that reaches x through the frozen experts is not computed; a
- * caller that has it passes it as dx_in.
+ * dW_r, db_r and the auxiliary loss need nothing else. The gradient that reaches x
+ * through the frozen experts is not computed: dg, and dh beyond dh_in, are the
+ * sublayer's only if the caller passes that share as dx_in; without it they hold
+ * the path through the logits alone, and the gain and what lies before the
+ * sublayer cannot be trained on them.
  *
  * Shared by these entry points:
  * - T tokens, E, k and d within the range above (1 <= E <= 256, k <= min(E, 32),
@@ -512,14 +515,16 @@ MOE_API int moe_forward_launch_count(int E, int k, int T, int d, int I);
  *   streams with workspaces of their own may run at the same time, and each may
  *   be captured into a CUDA graph.
  * - A NaN or an infinity in a live token's inputs shows as NaN (or infinity) in
- *   the outputs that depend on it; a logits' gradient or a weight beyond bf16's
- *   largest value (3.39e38) may count as an infinity in moe_router_backward.
+ *   the outputs that depend on it; a logits' gradient beyond bf16's largest value
+ *   (3.39e38) may count as an infinity in moe_router_backward's dW.
  * - Every sum over tokens has a fixed order: the same call gives the same bits.
  */
 
 /*
  * Load-balance and z loss of a batch's router logits, with the per-expert
- * counts. Over the n live tokens, with p_t = softmax(logits_t) over all E:
+ * counts. (Even routing has balance 1 whatever k is; a coefficient chosen for a loss
+ * with f_e = counts_e / n is to be multiplied by k here.)
+ * Over the n live tokens, with p_t = softmax(logits_t) over all E:
  *   f_e = counts_e / (n k),  P_e = (1/n) sum_t p_{t,e},
  *   balance = E sum_e f_e P_e,  z = (1/n) sum_t lse(logits_t)^2,
  *   loss = balance_coef * balance + z_coef * z.

@@ -718,8 +718,10 @@ class MoELayer:
         it reads lies in the layer's workspace): fills grads from dout bf16 [T, d],
         the gradient of out, and returns dh bf16 [T, d]. The auxiliary loss
         balance_coef * balance + z_coef * z is weighted by dloss (f32 [1]; None: 1).
-        The experts are frozen; their share of the gradient that reaches
-        RMSNorm(h), if the caller has it, is dx_in bf16 [T, d]."""
+        dW_r and db_r are complete. The experts are frozen, and their share of the
+        gradient that reaches RMSNorm(h) is not computed here: dh and grads.dg are the
+        sublayer's only if the caller passes it as dx_in bf16 [T, d]; without it they
+        hold the residual's gradient (dh) and the path through the logits."""
         T = dout.shape[0]
         if T > grads.T:
             raise ValueError("more tokens than the gradients' buffers were sized for")
