@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kBalWarps * 32) balance_partial_kernel(
 }
 
 // cols: E rounded up to a power of two; thread (share, e) adds every
-// (1024 / cols)-th cluster's row, at most nine.
+// (1024 / cols)-th cluster's row, at most eight (32 clusters, four shares at least).
 __global__ void __launch_bounds__(1024) balance_finish_kernel(BalanceScratch sc, int clusters, int E,
                                                               int cols, int k, BalanceOut out) {
   pdl_wait_and_trigger();

@@ -115,3 +115,28 @@ def test_backward_block_takes_the_experts_share(T):
     full = rstd[:, None] * (u + nn * (u * nn).mean(1, keepdims=True)) + np.abs(dout)
     close(val(dh.cpu().numpy()), dh64, (1 + BF16) * move + BF16 * np.abs(dh64) + 72 * U * full, "dh")
     close(f64(gr.dg), dg64, (tdx * nn).sum(0) + chain(T) * U * (u / np.abs(g) * nn).sum(0), "dg")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [24, 700])
+def test_backward_blocks_loss_is_the_operators(T):
+    """The step's loss, counts and shares have the bits of moe_balance_loss on the logits
+    and choices that the forward pass left."""
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from sparse_moe_layer_05_b200 import binding as B
+    from sparse_moe_layer_05_b200 import build
+    build.build()
+    from tests.test_gpu_router_train_step import A, B_Z, make_step, run_step
+    E, k = 8, 2
+    s = make_step(352, 224, E, k, T, seed=62)
+    run_step(s)
+    layer, gr = s["layer"], s["gr"]
+    other = B.RouterGrads(E, k, T, 352)
+    B.moe_balance_loss(layer.intermediate("logits", T), layer.intermediate("topk_idx", T), E, k, T, A, B_Z,
+                       other.stats, other.counts, other.mean_probs, other.lse, other.workspace,
+                       token_mask=s["t"]["mask"])
+    torch.cuda.synchronize()
+    for name in ("stats", "counts", "mean_probs", "lse"):
+        assert torch.equal(getattr(gr, name), getattr(other, name)), name

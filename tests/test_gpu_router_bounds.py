@@ -65,7 +65,8 @@ def test_dx_rounds_as_an_fp32_products(T, E, d):
 
 
 @pytest.mark.parametrize("with_in", [False, True])
-@pytest.mark.parametrize("T,E,d", [(150, 3, 64), (700, 20, 96), (400, 100, 320), (300, 200, 64)])
+@pytest.mark.parametrize("T,E,d", [(1000, 1, 64), (150, 2, 32), (150, 3, 64), (700, 20, 96), (400, 100, 320),
+                                   (300, 200, 64)])
 def test_dx_of_sizes_far_apart(T, E, d, with_in):
     """Tokens whose gradients lie between fp32's smallest subnormal and 2^100, each
     token's over 60 powers of two; weights over 40; whole rows of zeros."""
