@@ -104,17 +104,13 @@ __device__ __forceinline__ Terms split3(float v) {
   return t;
 }
 
-struct HalfTerms {
-  __half hi, mid;
-};
-__device__ __forceinline__ HalfTerms split2h(float v) {
-  HalfTerms t;
-  t.hi = __float2half_rn(v);
-  t.mid = __float2half_rn(v - __half2float(t.hi));
-  return t;
-}
-__device__ __forceinline__ uint32_t pack2(__half a, __half b) {
-  return __half_as_ushort(a) | (static_cast<uint32_t>(__half_as_ushort(b)) << 16);
+// Two values' fp16 terms, the first in the lower halves.
+__device__ __forceinline__ void split2h(float a, float b, uint32_t& hi, uint32_t& mid) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 f = __half22float2(h);
+  const __half2 m = __floats2half2_rn(a - f.x, b - f.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  mid = *reinterpret_cast<const uint32_t*>(&m);
 }
 // |v|, or 0 for what is no finite number: infinities and NaNs set no scale.
 __device__ __forceinline__ float finite_size(float v) {
@@ -221,10 +217,11 @@ __global__ void __launch_bounds__(256) router_terms_kernel(const float* __restri
         if (t >= t1 || !stores) continue;
         const int ex = half_scale(__uint_as_float(top[k]));
         const float up = exp2_int(ex);
-        const HalfTerms u = split2h(a[k] * up), v = split2h(b[k] * up);
+        uint32_t hi, mid;
+        split2h(a[k] * up, b[k] * up, hi, mid);
         const size_t at = static_cast<size_t>(t) * 64;
-        *reinterpret_cast<uint32_t*>(mid_x + at) = pack2(u.mid, v.mid);
-        *reinterpret_cast<uint32_t*>(hi_x + at) = pack2(u.hi, v.hi);
+        *reinterpret_cast<uint32_t*>(mid_x + at) = mid;
+        *reinterpret_cast<uint32_t*>(hi_x + at) = hi;
         if (pair == 0) exps[t] = static_cast<int8_t>(ex);
       }
     }
@@ -877,11 +874,7 @@ __global__ void __launch_bounds__(kDxThreads, 1)
     if (e >= a.p.ep) continue;
     uint32_t hi[4], mid[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const HalfTerms p = split2h(w[n][2 * j] * up), q = split2h(w[n][2 * j + 1] * up);
-      hi[j] = pack2(p.hi, q.hi);
-      mid[j] = pack2(p.mid, q.mid);
-    }
+    for (int j = 0; j < 4; ++j) split2h(w[n][2 * j] * up, w[n][2 * j + 1] * up, hi[j], mid[j]);
     uint8_t* blk = smem + (ch >> 3) * wblock;
     const uint32_t at = ((ch & 7) ^ (e & 7)) << 4;     // ep is a multiple of 8
     *reinterpret_cast<uint4*>(blk + e * 128 + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -988,25 +981,33 @@ __global__ void __launch_bounds__(kDxThreads, 1)
   } else if (warp >= 4 && warp < 4 + kOutWarps) {
     const int quad = warp & 3, half = (warp - 4) >> 2, r = quad * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    // the exponent and the mask's byte of the lane's token in unit q, loaded a unit ahead
+    // the exponent and the mask's byte of the lane's token in tile j, loaded a tile ahead
     uint32_t next_live = 1;
     int next_k = 0;
-    auto load_token = [&](int q) {
-      const int64_t t = static_cast<int64_t>(tile_row(q / units)) + r;
-      if (q >= n * units || t >= a.T) return;
+    auto load_token = [&](int j) {
+      const int64_t t = static_cast<int64_t>(tile_row(j)) + r;
+      if (j >= n || t >= a.T) return;
       next_k = __ldg(a.exps + t);
       if (MASKED) next_live = __ldg(a.mask + t);
     };
-    load_token(half);
+    // the group's tiles: all, or with one unit a tile every second
+    const int first = units > 1 ? 0 : half, stride = units > 1 ? 1 : 2;
+    load_token(first);
     // this group's units, counted over all tiles: half, half + 2, ...
-    int waited = -1;
+    int waited = -1, have = -1;
+    bool live = true;
+    float f0 = 1.f, f1 = 1.f;
     for (int q = half; q < n * units; q += 2) {
       const int j = q / units, u = q % units, b = j & 1, s = q % a.staging;
-      const bool live = next_live != 0;
-      // 2^-(the terms' exponents) as two factors: one alone may pass fp32's range
-      const int k = -(next_k + kw);
-      const float f0 = exp2_int(k >> 1), f1 = exp2_int(k - (k >> 1));
-      load_token(q + 2);
+      if (j != have) {
+        have = j;
+        live = next_live != 0;
+        // 2^-(the terms' exponents) as two factors: one alone may pass fp32's range
+        const int k = -(next_k + kw);
+        f0 = exp2_int(k >> 1);
+        f1 = exp2_int(k - (k >> 1));
+        load_token(j + stride);
+      }
       for (; waited < j; ++waited)
         if ((units > 1 || ((waited + 1) & 1) == half) &&
             !warp_wait(bar_acc((waited + 1) & 1), (waited + 1) >> 1 & 1, abort_flag, a.status))
@@ -1038,9 +1039,9 @@ __global__ void __launch_bounds__(kDxThreads, 1)
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const __nv_bfloat162 z = __floats2bfloat162_rn(
-                fmaf(__uint_as_float(v[8 * h + 2 * k]) * f0, f1, __uint_as_float(w[k] << 16)),
-                fmaf(__uint_as_float(v[8 * h + 2 * k + 1]) * f0, f1, __uint_as_float(w[k] & 0xFFFF0000u)));
+            const float2 y = make_float2(__uint_as_float(v[8 * h + 2 * k]), __uint_as_float(v[8 * h + 2 * k + 1]));
+            const float2 sum = fma2(mul2(y, both(f0)), both(f1), bf16_pair(w[k]));
+            const __nv_bfloat162 z = __floats2bfloat162_rn(sum.x, sum.y);
             w[k] = *reinterpret_cast<const uint32_t*>(&z);
           }
           // a padded token's row stays dx_in's (its sum may be zero times an infinity)
