@@ -663,10 +663,11 @@ __global__ void __launch_bounds__(256) router_small_kernel(const SmallArgs a) {
   }
 }
 
-// Which path. Measured, one launch against the tensor cores (d = 2880 unless said):
-// E = 32: T = 128 8.7 against 10.5 us, T = 192 11.6 against 10.7; E = 4, d = 512:
-// T = 128 7.3 against 9.0, T = 192 10.4 against 9.4; E = 128: T = 64 11.5 against
-// 17, T = 128 19.6 against 17.7.
+// Which path. Measured, one launch against the tensor cores (bf16 rows, d = 2880
+// unless said): E = 4, d = 512: T = 144 9.0 against 11.3 us, T = 192 10.6 against
+// 10.3; E = 32: 9.8 against 12.1 and 11.4 against 12.0; E = 64: 13.7 against 15.2
+// and 16.2 against 15.4; E = 128: T = 64 10.9 against 15.7, T = 96 17.0 against 16.3,
+// T = 128 18.7 against 16.4; E = 248: T = 64 21.2 against 19.6, T = 96 29 against 20.
 bool few_tokens(int E, int T, int d) { return T <= (static_cast<int64_t>(E) * d > 1 << 18 ? 96 : 144); }
 
 }  // namespace
